@@ -22,7 +22,9 @@ STATUS_NAMES = {
 EXPORTS = ("bsa_pool", "bsa_compress_select", "bsa_compress_select_ws", "bsa_fine_attention",
            "bsa_workspace_size", "bsa_forward", "bsa_check_status", "bsa_status_string", "bsa_forward_noalloc",
            "bsa_forward_train", "bsa_backward_workspace_size", "bsa_backward", "bsa_permute_tokens",
-           "bsa_latlon_healpix_plan", "bsa_latlon_workspace_size", "bsa_latlon_to_healpix", "bsa_forward_mirrored")
+           "bsa_latlon_healpix_plan", "bsa_latlon_workspace_size", "bsa_latlon_to_healpix", "bsa_forward_mirrored",
+           "bsa_cross_workspace_size", "bsa_cross_attention", "bsa_cross_backward_workspace_size",
+           "bsa_cross_attention_backward", "bsa_prefix_workspace_size", "bsa_prefix_attention")
 TESTING_EXPORTS = ("bsa_testing_fine_attention_withhold", "bsa_testing_exp2", "bsa_testing_mma_rate")
 
 
@@ -30,6 +32,19 @@ class BsaConfig(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32), ("top_n", ctypes.c_int32),
                 ("window_blocks", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class BsaCrossConfig(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("n_q", ctypes.c_int32), ("n_k", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class BsaPrefixConfig(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("groups", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("n_q", ctypes.c_int32), ("n_prefix", ctypes.c_int32),
+                ("n_own", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
 
 
 class BsaError(RuntimeError):
@@ -50,6 +65,7 @@ def load() -> ctypes.CDLL:
         raise ImportError(f"libbsa.so is not built ({LIB_PATH}); run python -m block_sparse_spherical_b200.build")
     lib = ctypes.CDLL(LIB_PATH)
     P, S, C = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(BsaConfig)
+    X, Y = ctypes.POINTER(BsaCrossConfig), ctypes.POINTER(BsaPrefixConfig)
     sig = {
         "bsa_pool": [C, P, P, P, P, P, P, P],
         "bsa_compress_select": [C, P, P, P, P, P, P],
@@ -69,6 +85,12 @@ def load() -> ctypes.CDLL:
         "bsa_latlon_workspace_size": [ctypes.c_int64, ctypes.c_int64, ctypes.POINTER(ctypes.c_size_t)],
         "bsa_latlon_to_healpix": [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
                                   ctypes.c_float, P, P, P, P, P, P, P, S, P, P],
+        "bsa_cross_workspace_size": [X, ctypes.POINTER(ctypes.c_size_t)],
+        "bsa_cross_attention": [X, P, P, P, P, P, P, P, S, P, P],
+        "bsa_cross_backward_workspace_size": [X, ctypes.POINTER(ctypes.c_size_t)],
+        "bsa_cross_attention_backward": [X, P, P, P, P, P, P, P, P, P, P, P, S, P, P],
+        "bsa_prefix_workspace_size": [Y, ctypes.POINTER(ctypes.c_size_t)],
+        "bsa_prefix_attention": [Y, P, P, P, P, P, P, P, P, P, S, P, P],
         "bsa_testing_fine_attention_withhold": [C, P, P, P, P, P, P, P, P, ctypes.c_int64, P],
         "bsa_testing_exp2": [P, P, ctypes.c_int64, ctypes.c_int32, P],
         "bsa_testing_mma_rate": [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P],
@@ -209,6 +231,46 @@ def bsa_forward_mirrored(cfg: BsaConfig, q, k, v, gates, out, mirrors, sel_idx_o
     _check("bsa_forward_mirrored", load().bsa_forward_mirrored(
         ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(gates), _ptr(out), arr, len(mirrors),
         _ptr(sel_idx_out), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def bsa_cross_workspace_size(cfg: BsaCrossConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check("bsa_cross_workspace_size", load().bsa_cross_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def bsa_cross_attention(cfg: BsaCrossConfig, q, k, v, key_len, out, lse, workspace, workspace_bytes: int,
+                        status_word=None, stream=None) -> None:
+    _check("bsa_cross_attention", load().bsa_cross_attention(
+        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(key_len), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace_bytes, _ptr(status_word), _stream(stream)))
+
+
+def bsa_cross_backward_workspace_size(cfg: BsaCrossConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check("bsa_cross_backward_workspace_size",
+           load().bsa_cross_backward_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def bsa_cross_attention_backward(cfg: BsaCrossConfig, q, k, v, key_len, out, lse, dout, dq, dk, dv, workspace,
+                                 workspace_bytes: int, status_word=None, stream=None) -> None:
+    _check("bsa_cross_attention_backward", load().bsa_cross_attention_backward(
+        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(key_len), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
+        _ptr(dk), _ptr(dv), _ptr(workspace), workspace_bytes, _ptr(status_word), _stream(stream)))
+
+
+def bsa_prefix_workspace_size(cfg: BsaPrefixConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check("bsa_prefix_workspace_size", load().bsa_prefix_workspace_size(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def bsa_prefix_attention(cfg: BsaPrefixConfig, q, k_prefix, v_prefix, prefix_len, k_own, v_own, own_len, out,
+                         workspace, workspace_bytes: int, status_word=None, stream=None) -> None:
+    _check("bsa_prefix_attention", load().bsa_prefix_attention(
+        ctypes.byref(cfg), _ptr(q), _ptr(k_prefix), _ptr(v_prefix), _ptr(prefix_len), _ptr(k_own), _ptr(v_own),
+        _ptr(own_len), _ptr(out), _ptr(workspace), workspace_bytes, _ptr(status_word), _stream(stream)))
 
 
 def bsa_testing_mma_rate(m: int, n: int, warps: int, cycles, stream=None) -> None:

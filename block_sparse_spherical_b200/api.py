@@ -231,6 +231,163 @@ class LatLonToHealpix:
         return out
 
 
+class _DenseLayer:
+    """What the layers of fixed sizes below share: their device, status word and calls on it.
+
+    A call runs on the layer's device and that device's current stream, whichever device is current.
+    Workspaces come from torch's allocator anew in each call (on that stream, or from a capturing
+    graph's own pool), so that one layer may be called from several streams and graphs at once.
+    """
+
+    def __init__(self, batch, heads, kv_heads, head_dim, dtype, scale, device):
+        if dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"dtype must be bfloat16, got {dtype}")
+        self.kv_heads = heads if kv_heads is None else kv_heads
+        self.dtype, self.scale = dtype, scale
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.device = self.status.device
+        if not self.status.is_cuda:
+            raise ValueError(f"the layer needs a CUDA device, got {device}")
+        self._code = abi.BSA_BF16 if dtype == torch.bfloat16 else abi.BSA_F32
+
+    def _take(self, t, name, shape, dtype=None):
+        _require(t, name, self.dtype if dtype is None else dtype, shape)
+        if t.device != self.device:
+            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+
+    def _lengths(self, t, name, count):
+        if t is not None:
+            self._take(t, name, (count,), torch.int32)
+
+    def _workspace(self, nbytes):
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
+
+    def _on_device(self, call, *args):
+        stream = torch.cuda.current_stream(self.device).cuda_stream
+        if torch.cuda.current_device() == self.device.index:
+            call(*args, self.status, stream)
+        else:
+            with torch.cuda.device(self.device):
+                call(*args, self.status, stream)
+
+    def check_status(self) -> int:
+        """Synchronise and return the kernels' status code (0 = OK); resets it."""
+        with torch.cuda.device(self.device):
+            return abi.bsa_check_status(self.status)
+
+
+class CrossAttention(_DenseLayer):
+    """Attention of n_q query rows a head to an encoder's n_k states (include/bsa.h: bsa_cross_attention).
+
+    Calling the object with q [B, H, n_q, d], k and v [B, H_kv, n_k, d] (bf16, d 64 or 128, H a multiple
+    of H_kv) and, for a padded batch, key_len [B] (int32, 0 to n_k) returns out [B, H, n_q, d]. States
+    behind key_len are never used; a batch entry without states gives zero rows.
+    """
+
+    def __init__(self, batch: int, heads: int, n_q: int, n_k: int, head_dim: int, kv_heads: int | None = None,
+                 dtype=torch.bfloat16, scale: float = 0.0, device="cuda"):
+        super().__init__(batch, heads, kv_heads, head_dim, dtype, scale, device)
+        self.cfg = abi.BsaCrossConfig(batch, heads, self.kv_heads, n_q, n_k, head_dim, self._code, scale)
+        self.workspace_bytes = abi.bsa_cross_workspace_size(self.cfg)
+        self.batch = batch
+        self.shape = (batch, heads, n_q, head_dim)
+        self.kv_shape = (batch, self.kv_heads, n_k, head_dim)
+
+    def _forward(self, q, k, v, key_len, out, lse):
+        self._take(q, "q", self.shape)
+        self._take(k, "k", self.kv_shape)
+        self._take(v, "v", self.kv_shape)
+        self._lengths(key_len, "key_len", self.batch)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._take(out, "out", self.shape)
+        self._on_device(abi.bsa_cross_attention, self.cfg, q, k, v, key_len, out, lse,
+                        self._workspace(self.workspace_bytes), self.workspace_bytes)
+        return out
+
+    def __call__(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
+        return self._forward(q, k, v, key_len, out, None)
+
+
+class CrossAttentionTrain(CrossAttention):
+    """A CrossAttention layer for training.
+
+    forward(q, k, v, key_len) -> out; backward(dout) -> (dq, dk, dv) of the last forward(). Its q, k, v,
+    key_len and out are kept by reference until then and have to stay as they are.
+    """
+
+    def __init__(self, *args, **kw):
+        super().__init__(*args, **kw)
+        self.bwd_workspace_bytes = abi.bsa_cross_backward_workspace_size(self.cfg)
+        self._saved = None
+
+    def __call__(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
+        return self.forward(q, k, v, key_len, out)
+
+    def forward(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
+        lse = torch.empty(self.shape[:3], dtype=torch.float32, device=self.device)
+        out = self._forward(q, k, v, key_len, out, lse)
+        self._saved = (q, k, v, key_len, out, lse)
+        return out
+
+    def backward(self, dout, grads=None):
+        """Gradients (dq, dk, dv) of the last forward() for dL/dout = dout."""
+        if self._saved is None:
+            raise RuntimeError("backward() needs a forward() first")
+        q, k, v, key_len, out, lse = self._saved
+        self._take(dout, "dout", self.shape)
+        if grads is None:
+            grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
+        else:
+            for t, name, shape in zip(grads, ("dq", "dk", "dv"), (self.shape, self.kv_shape, self.kv_shape)):
+                self._take(t, name, shape)
+        dq, dk, dv = grads
+        self._on_device(abi.bsa_cross_attention_backward, self.cfg, q, k, v, key_len, out, lse, dout, dq, dk, dv,
+                        self._workspace(self.bwd_workspace_bytes), self.bwd_workspace_bytes)
+        return dq, dk, dv
+
+
+class PrefixAttention(_DenseLayer):
+    """Attention of an ensemble's members to a prefix they share and to states of their own, in one
+    softmax (include/bsa.h: bsa_prefix_attention).
+
+    The batch is `groups` ensembles of batch / groups consecutive members. Calling the object with q
+    [B, H, n_q, d], k_prefix and v_prefix [groups, H_kv, n_prefix, d], k_own and v_own [B, H_kv, n_own, d]
+    (bf16) and, where buffers are not full, prefix_len [groups] and own_len [B] (int32, 0 allowed) returns
+    [B, H, n_q, d]. The prefix is read once for a group's members together.
+    """
+
+    def __init__(self, batch: int, heads: int, n_q: int, n_prefix: int, n_own: int, head_dim: int,
+                 kv_heads: int | None = None, groups: int = 1, dtype=torch.bfloat16, scale: float = 0.0,
+                 device="cuda"):
+        super().__init__(batch, heads, kv_heads, head_dim, dtype, scale, device)
+        self.cfg = abi.BsaPrefixConfig(batch, groups, heads, self.kv_heads, n_q, n_prefix, n_own, head_dim,
+                                       self._code, scale)
+        self.workspace_bytes = abi.bsa_prefix_workspace_size(self.cfg)
+        self.batch, self.groups = batch, groups
+        self.shape = (batch, heads, n_q, head_dim)
+        self.prefix_shape = (groups, self.kv_heads, n_prefix, head_dim)
+        self.own_shape = (batch, self.kv_heads, n_own, head_dim)
+
+    def __call__(self, q, k_prefix, v_prefix, k_own, v_own, prefix_len=None, own_len=None,
+                 out=None) -> torch.Tensor:
+        self._take(q, "q", self.shape)
+        self._take(k_prefix, "k_prefix", self.prefix_shape)
+        self._take(v_prefix, "v_prefix", self.prefix_shape)
+        self._take(k_own, "k_own", self.own_shape)
+        self._take(v_own, "v_own", self.own_shape)
+        self._lengths(prefix_len, "prefix_len", self.groups)
+        self._lengths(own_len, "own_len", self.batch)
+        if out is None:
+            out = torch.empty_like(q)
+        else:
+            self._take(out, "out", self.shape)
+        self._on_device(abi.bsa_prefix_attention, self.cfg, q, k_prefix, v_prefix, prefix_len, k_own, v_own, own_len,
+                        out, self._workspace(self.workspace_bytes), self.workspace_bytes)
+        return out
+
+
 def forward(q, k, v, gates, block_size: int, top_n: int, window_blocks: int = 1, scale: float = 0.0,
             return_indices: bool = False):
     """One-shot BSA forward (allocates a workspace; use BSA for repeated calls)."""

@@ -1,0 +1,157 @@
+// C ABI of cross attention, its backward and shared-prefix attention (declared
+// in include/bsa.h): argument validation, workspace layout and dispatch. No
+// allocation, no synchronisation, no global state.
+#include <math.h>
+
+#include "cross.cuh"
+
+namespace {
+
+using bsa::DenseProblem;
+using bsa::KeySet;
+
+constexpr int64_t kMaxRows = 0x7fffff00LL;   // row coordinates are int32, tiles round up
+
+bool aligned(const void *p, uintptr_t n) { return ((uintptr_t)p & (n - 1)) == 0; }
+
+bsa_status make_dense(int32_t batch, int32_t heads, int32_t kv_heads, int32_t n_q, int32_t head_dim, int32_t dtype,
+                      float scale, DenseProblem *p) {
+    if (batch < 1 || heads < 1 || kv_heads < 1 || n_q < 1 || head_dim < 1 || heads % kv_heads != 0)
+        return BSA_ERR_INVALID_ARG;
+    if (dtype != BSA_F32 && dtype != BSA_BF16) return BSA_ERR_INVALID_ARG;
+    if (!(scale >= 0.0f) || isinf(scale)) return BSA_ERR_INVALID_ARG;
+    if (dtype != BSA_BF16 || (head_dim != 64 && head_dim != 128)) return BSA_ERR_UNSUPPORTED;
+    p->batch = batch;
+    p->heads = heads;
+    p->kv_heads = kv_heads;
+    p->n_q = n_q;
+    p->d = head_dim;
+    p->rows = (int64_t)(heads / kv_heads) * n_q;
+    p->scale = scale > 0.0f ? scale : 1.0f / sqrtf((float)head_dim);
+    // slabs are a TMA coordinate; rows of a slab too
+    if (p->rows > kMaxRows || (int64_t)batch * kv_heads > kMaxRows) return BSA_ERR_UNSUPPORTED;
+    return BSA_OK;
+}
+
+bsa_status make_cross(const bsa_cross_config *c, DenseProblem *p) {
+    if (!c || c->n_k < 1) return BSA_ERR_INVALID_ARG;
+    const bsa_status st = make_dense(c->batch, c->heads, c->kv_heads, c->n_q, c->head_dim, c->dtype, c->scale, p);
+    return st != BSA_OK ? st : (c->n_k > kMaxRows ? BSA_ERR_UNSUPPORTED : BSA_OK);
+}
+
+bsa_status make_prefix(const bsa_prefix_config *c, DenseProblem *p) {
+    if (!c || c->n_prefix < 1 || c->n_own < 1 || c->groups < 1) return BSA_ERR_INVALID_ARG;
+    if (c->batch < 1 || c->batch % c->groups != 0) return BSA_ERR_INVALID_ARG;
+    const bsa_status st = make_dense(c->batch, c->heads, c->kv_heads, c->n_q, c->head_dim, c->dtype, c->scale, p);
+    return st != BSA_OK ? st : (c->n_prefix > kMaxRows || c->n_own > kMaxRows ? BSA_ERR_UNSUPPORTED : BSA_OK);
+}
+
+bsa_status from_cuda(cudaError_t e) {
+    if (e == cudaSuccess) return BSA_OK;
+    return e == cudaErrorNotSupported ? BSA_ERR_UNSUPPORTED : BSA_ERR_CUDA;
+}
+
+bsa_status check_workspace(const void *workspace, size_t have, size_t need) {
+    if (need == 0) return BSA_OK;
+    if (!workspace || have < need) return BSA_ERR_WORKSPACE;
+    return aligned(workspace, 256) ? BSA_OK : BSA_ERR_ALIGNMENT;
+}
+
+}  // namespace
+
+extern "C" {
+
+bsa_status bsa_cross_workspace_size(const bsa_cross_config *cfg, size_t *bytes) {
+    DenseProblem p;
+    const bsa_status st = make_cross(cfg, &p);
+    if (st != BSA_OK) return st;
+    if (!bytes) return BSA_ERR_INVALID_ARG;
+    *bytes = 0;
+    return BSA_OK;
+}
+
+bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
+                               const int32_t *key_len, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                               uint32_t *status_word, cudaStream_t stream) {
+    DenseProblem p;
+    const bsa_status st = make_cross(cfg, &p);
+    if (st != BSA_OK) return st;
+    if (!q || !k || !v || !out) return BSA_ERR_INVALID_ARG;
+    if (out == q || out == k || out == v) return BSA_ERR_INVALID_ARG;
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, 0);
+    if (ws != BSA_OK) return ws;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
+        !aligned(key_len, 4) || !aligned(status_word, 4))
+        return BSA_ERR_ALIGNMENT;
+    const KeySet s{k, v, key_len, cfg->n_k, p.batch, 1}, none{};
+    return from_cuda(bsa::launch_dense_fwd(p, q, s, none, out, lse, status_word, stream));
+}
+
+bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t *bytes) {
+    DenseProblem p;
+    const bsa_status st = make_cross(cfg, &p);
+    if (st != BSA_OK) return st;
+    if (!bytes) return BSA_ERR_INVALID_ARG;
+    *bytes = 0;
+    return BSA_OK;
+}
+
+bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
+                                        const int32_t *key_len, const void *out, const float *lse, const void *dout,
+                                        void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes,
+                                        uint32_t *status_word, cudaStream_t stream) {
+    DenseProblem p;
+    const bsa_status st = make_cross(cfg, &p);
+    if (st != BSA_OK) return st;
+    const void *in[] = {q, k, v, out, dout, lse};
+    void *grads[] = {dq, dk, dv};
+    for (const void *x : in)
+        if (!x) return BSA_ERR_INVALID_ARG;
+    for (int i = 0; i < 3; ++i) {
+        if (!grads[i] || grads[i] == grads[(i + 1) % 3]) return BSA_ERR_INVALID_ARG;
+        for (const void *x : in)
+            if (x == grads[i]) return BSA_ERR_INVALID_ARG;
+    }
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, 0);
+    if (ws != BSA_OK) return ws;
+    for (int i = 0; i < 5; ++i)
+        if (!aligned(in[i], 16)) return BSA_ERR_ALIGNMENT;
+    if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4) || !aligned(key_len, 4) ||
+        !aligned(status_word, 4))
+        return BSA_ERR_ALIGNMENT;
+    const KeySet s{k, v, key_len, cfg->n_k, p.batch, 1};
+    return from_cuda(bsa::launch_dense_bwd(p, q, s, out, lse, dout, dq, dk, dv, status_word, stream));
+}
+
+bsa_status bsa_prefix_workspace_size(const bsa_prefix_config *cfg, size_t *bytes) {
+    DenseProblem p;
+    const bsa_status st = make_prefix(cfg, &p);
+    if (st != BSA_OK) return st;
+    if (!bytes) return BSA_ERR_INVALID_ARG;
+    *bytes = 0;
+    return BSA_OK;
+}
+
+bsa_status bsa_prefix_attention(const bsa_prefix_config *cfg, const void *q, const void *k_prefix, const void *v_prefix,
+                                const int32_t *prefix_len, const void *k_own, const void *v_own, const int32_t *own_len,
+                                void *out, void *workspace, size_t workspace_bytes, uint32_t *status_word,
+                                cudaStream_t stream) {
+    DenseProblem p;
+    const bsa_status st = make_prefix(cfg, &p);
+    if (st != BSA_OK) return st;
+    const void *in[] = {q, k_prefix, v_prefix, k_own, v_own};
+    for (const void *x : in)
+        if (!x || x == out) return BSA_ERR_INVALID_ARG;
+    if (!out) return BSA_ERR_INVALID_ARG;
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, 0);
+    if (ws != BSA_OK) return ws;
+    for (const void *x : in)
+        if (!aligned(x, 16)) return BSA_ERR_ALIGNMENT;
+    if (!aligned(out, 16) || !aligned(prefix_len, 4) || !aligned(own_len, 4) || !aligned(status_word, 4))
+        return BSA_ERR_ALIGNMENT;
+    const KeySet pre{k_prefix, v_prefix, prefix_len, cfg->n_prefix, cfg->groups, p.batch / cfg->groups};
+    const KeySet own{k_own, v_own, own_len, cfg->n_own, p.batch, 1};
+    return from_cuda(bsa::launch_dense_fwd(p, q, pre, own, out, nullptr, status_word, stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,191 @@
+// Dense attention over states of another length on the CUDA cores, the plain
+// way: one warp a query row (forward, dq) or a key row (dk, dv), lane j holding
+// the j-th of 32 keys (rows) for the scores and d/32 channels for the sums.
+#include <math_constants.h>
+
+#include "cross.cuh"
+
+namespace bsa {
+namespace {
+
+constexpr int kWarps = 4;
+
+__device__ __forceinline__ int clamped_len(const int32_t *len, int64_t i, int64_t n, uint32_t *status) {
+    if (!len) return (int)n;
+    const int64_t x = __ldg(len + i);
+    if (x < 0 || x > n) {
+        if (status) atomicOr(status, kStatusBadIndex);
+        return x < 0 ? 0 : (int)n;
+    }
+    return (int)x;
+}
+
+template <int D>
+__device__ __forceinline__ float dot_row(const float *a, const __nv_bfloat16 *b) {
+    float s = 0.f;
+    for (int c = 0; c < D; c += 2) {
+        const float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(b + c));
+        s = fmaf(a[c], x.x, s);
+        s = fmaf(a[c + 1], x.y, s);
+    }
+    return s;
+}
+
+template <int D>
+__global__ void fwd_kernel(DenseProblem p, const __nv_bfloat16 *q, KeySet s0, KeySet s1, __nv_bfloat16 *out,
+                           float *lse, uint32_t *status) {
+    __shared__ float qs[kWarps][D];
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t row = (int64_t)blockIdx.x * kWarps + w;
+    if (row >= p.batch * p.kv_heads * p.rows) return;
+    const int64_t slab = row / p.rows, b = slab / p.kv_heads, hk = slab % p.kv_heads;
+    for (int c = lane; c < D; c += 32) qs[w][c] = __bfloat162float(q[row * D + c]) * p.scale;
+    __syncwarp();
+    float m = -CUDART_INF_F, l = 0.f, o[D / 32];
+    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
+    for (int part = 0; part < 2; ++part) {
+        const KeySet &s = part ? s1 : s0;
+        if (!s.k) continue;
+        const int64_t set = b / s.members, base = (set * p.kv_heads + hk) * s.n;
+        const int len = clamped_len(s.len, set, s.n, status);
+        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(s.k) + base * D;
+        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(s.v) + base * D;
+        for (int j0 = 0; j0 < len; j0 += 32) {
+            const int j = j0 + lane;
+            const float x = j < len ? dot_row<D>(qs[w], k + (int64_t)j * D) : -CUDART_INF_F;
+            float mx = x;
+            for (int i = 16; i; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, i));
+            const float mn = fmaxf(m, mx), a = m == mn ? 1.f : expf(m - mn);
+            const float pr = j < len ? expf(x - mn) : 0.f;
+            l = l * a + pr;
+            m = mn;
+            for (int e = 0; e < D / 32; ++e) o[e] *= a;
+            const int cnt = min(32, len - j0);
+            for (int jj = 0; jj < cnt; ++jj) {
+                const float pj = __shfl_sync(~0u, pr, jj);
+                for (int e = 0; e < D / 32; ++e)
+                    o[e] = fmaf(pj, __bfloat162float(v[(int64_t)(j0 + jj) * D + lane + 32 * e]), o[e]);
+            }
+        }
+    }
+    for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
+    for (int e = 0; e < D / 32; ++e) out[row * D + lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
+    if (lse && lane == 0) lse[row] = l == 0.f ? -CUDART_INF_F : m + logf(l);
+}
+
+// dq of one row: dq = s Σ_j p_j (dp_j - D) k_j
+template <int D>
+__global__ void dq_kernel(DenseProblem p, const __nv_bfloat16 *q, KeySet s, const __nv_bfloat16 *out, const float *lse,
+                          const __nv_bfloat16 *dout, __nv_bfloat16 *dq, uint32_t *status) {
+    __shared__ float qs[kWarps][D], os[kWarps][D];
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t row = (int64_t)blockIdx.x * kWarps + w;
+    if (row >= p.batch * p.kv_heads * p.rows) return;
+    const int64_t slab = row / p.rows, b = slab / p.kv_heads;
+    float dt = 0.f, acc[D / 32];
+    for (int e = 0; e < D / 32; ++e) {
+        const int c = lane + 32 * e;
+        acc[e] = 0.f;
+        qs[w][c] = __bfloat162float(q[row * D + c]) * p.scale;
+        os[w][c] = __bfloat162float(dout[row * D + c]);
+        dt = fmaf(os[w][c], __bfloat162float(out[row * D + c]), dt);
+    }
+    for (int i = 16; i; i >>= 1) dt += __shfl_xor_sync(~0u, dt, i);
+    __syncwarp();
+    const int len = clamped_len(s.len, b, s.n, status);
+    const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(s.k) + slab * s.n * D;
+    const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(s.v) + slab * s.n * D;
+    const float ls = lse[row];
+    for (int j0 = 0; j0 < len; j0 += 32) {
+        const int j = j0 + lane;
+        float ds = 0.f;
+        if (j < len) {
+            const float x = dot_row<D>(qs[w], k + (int64_t)j * D), dp = dot_row<D>(os[w], v + (int64_t)j * D);
+            ds = expf(x - ls) * (dp - dt);
+        }
+        const int cnt = min(32, len - j0);
+        for (int jj = 0; jj < cnt; ++jj) {
+            const float dj = __shfl_sync(~0u, ds, jj);
+            for (int e = 0; e < D / 32; ++e)
+                acc[e] = fmaf(dj, __bfloat162float(k[(int64_t)(j0 + jj) * D + lane + 32 * e]), acc[e]);
+        }
+    }
+    for (int e = 0; e < D / 32; ++e) dq[row * D + lane + 32 * e] = __float2bfloat16_rn(acc[e] * p.scale);
+}
+
+// dk, dv of one key: dv = Σ_i p_i do_i, dk = s Σ_i p_i (dp_i - D_i) q_i
+template <int D>
+__global__ void dkv_kernel(DenseProblem p, const __nv_bfloat16 *q, KeySet s, const __nv_bfloat16 *out,
+                           const float *lse, const __nv_bfloat16 *dout, __nv_bfloat16 *dk, __nv_bfloat16 *dv,
+                           uint32_t *status) {
+    __shared__ float ks[kWarps][D], vs[kWarps][D];
+    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t row = (int64_t)blockIdx.x * kWarps + w;
+    if (row >= p.batch * p.kv_heads * s.n) return;
+    const int64_t slab = row / s.n, b = slab / p.kv_heads;
+    const int len = clamped_len(s.len, b, s.n, status);
+    float ak[D / 32], av[D / 32];
+    for (int e = 0; e < D / 32; ++e) ak[e] = av[e] = 0.f;
+    if (row % s.n < len) {
+        for (int c = lane; c < D; c += 32) {
+            ks[w][c] = __bfloat162float(static_cast<const __nv_bfloat16 *>(s.k)[row * D + c]) * p.scale;
+            vs[w][c] = __bfloat162float(static_cast<const __nv_bfloat16 *>(s.v)[row * D + c]);
+        }
+        __syncwarp();
+        const int64_t r0 = slab * p.rows;
+        for (int64_t i0 = 0; i0 < p.rows; i0 += 32) {
+            const int64_t i = i0 + lane;
+            float pr = 0.f, ds = 0.f;
+            if (i < p.rows) {
+                const __nv_bfloat16 *qi = q + (r0 + i) * D, *oi = dout + (r0 + i) * D, *yi = out + (r0 + i) * D;
+                float dt = 0.f;
+                for (int c = 0; c < D; ++c) dt = fmaf(__bfloat162float(oi[c]), __bfloat162float(yi[c]), dt);
+                pr = expf(dot_row<D>(ks[w], qi) - lse[r0 + i]);
+                ds = pr * (dot_row<D>(vs[w], oi) - dt);
+            }
+            const int cnt = (int)min((int64_t)32, p.rows - i0);
+            for (int ii = 0; ii < cnt; ++ii) {
+                const float pi = __shfl_sync(~0u, pr, ii), di = __shfl_sync(~0u, ds, ii);
+                for (int e = 0; e < D / 32; ++e) {
+                    const int64_t at = (r0 + i0 + ii) * D + lane + 32 * e;
+                    av[e] = fmaf(pi, __bfloat162float(dout[at]), av[e]);
+                    ak[e] = fmaf(di, __bfloat162float(q[at]), ak[e]);
+                }
+            }
+        }
+    }
+    for (int e = 0; e < D / 32; ++e) {
+        dk[row * D + lane + 32 * e] = __float2bfloat16_rn(ak[e] * p.scale);
+        dv[row * D + lane + 32 * e] = __float2bfloat16_rn(av[e]);
+    }
+}
+
+using bf = __nv_bfloat16;
+unsigned ctas(int64_t rows) { return (unsigned)((rows + kWarps - 1) / kWarps); }
+
+}  // namespace
+
+cudaError_t launch_dense_fwd(const DenseProblem &p, const void *q, const KeySet &s0, const KeySet &s1, void *out,
+                             float *lse, uint32_t *status, cudaStream_t stream) {
+    const int64_t rows = p.batch * p.kv_heads * p.rows;
+    auto kern = p.d == 64 ? fwd_kernel<64> : fwd_kernel<128>;
+    kern<<<ctas(rows), 32 * kWarps, 0, stream>>>(p, static_cast<const bf *>(q), s0, s1, static_cast<bf *>(out), lse,
+                                                 status);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_dense_bwd(const DenseProblem &p, const void *q, const KeySet &s, const void *out, const float *lse,
+                             const void *dout, void *dq, void *dk, void *dv, uint32_t *status, cudaStream_t stream) {
+    const int64_t rows = p.batch * p.kv_heads * p.rows, keys = p.batch * p.kv_heads * s.n;
+    auto kq = p.d == 64 ? dq_kernel<64> : dq_kernel<128>;
+    kq<<<ctas(rows), 32 * kWarps, 0, stream>>>(p, static_cast<const bf *>(q), s, static_cast<const bf *>(out), lse,
+                                               static_cast<const bf *>(dout), static_cast<bf *>(dq), status);
+    auto kk = p.d == 64 ? dkv_kernel<64> : dkv_kernel<128>;
+    kk<<<ctas(keys), 32 * kWarps, 0, stream>>>(p, static_cast<const bf *>(q), s, static_cast<const bf *>(out), lse,
+                                               static_cast<const bf *>(dout), static_cast<bf *>(dk),
+                                               static_cast<bf *>(dv), status);
+    return cudaGetLastError();
+}
+
+}  // namespace bsa

@@ -63,7 +63,8 @@ typedef enum {
     BSA_ERR_CUDA = 4,         /* a CUDA runtime call or kernel launch failed */
     BSA_ERR_TIMEOUT = 5,      /* a kernel's bounded wait expired (reported via the status word) */
     BSA_ERR_WORKSPACE = 6,    /* workspace missing or smaller than bsa_workspace_size() */
-    BSA_ERR_INDEX = 7         /* a kernel met a block index outside [0, m) (via the status word) */
+    BSA_ERR_INDEX = 7         /* a kernel met a block index outside [0, m), or a length outside its buffer
+                                 (via the status word) */
 } bsa_status;
 
 typedef enum { BSA_F32 = 0, BSA_BF16 = 1 } bsa_dtype;
@@ -304,6 +305,101 @@ BSA_API bsa_status bsa_backward(const bsa_config *cfg, const void *q, const void
 BSA_API bsa_status bsa_forward_noalloc(const bsa_config *cfg, const void *q, const void *k, const void *v,
                                        const float *gates, void *out, int32_t *sel_idx_out,
                                        uint32_t *status_word, cudaStream_t stream);
+
+/*
+ * Cross attention to an encoder's states of another length: every query row
+ * attends to all states of its batch entry, without a causal order,
+ *   o_i = Σ_{j < len} p_ij v_j,  p_ij = softmax_j(s·q_i·k_j)
+ * (the dense counterpart of the interpolation's neighbour attention: HEALPix
+ * tokens against a coarser trunk's states, or against a whole lat-lon field).
+ *
+ * Layouts, contiguous, bf16 (lengths int32, lse float):
+ *   q, out   [batch][heads][n_q][head_dim]
+ *   k, v     [batch][kv_heads][n_k][head_dim]; heads is a multiple of kv_heads
+ *            and query head h reads key head h / (heads / kv_heads)
+ *   key_len  [batch], nullable (all n_k): entry b attends to its first
+ *            key_len[b] states; what lies behind them is never used, whatever
+ *            it holds (NaN included). A length of 0 gives zero rows with
+ *            lse = -inf and no gradient. A length outside [0, n_k] is clamped
+ *            and flagged BSA_ERR_INDEX in *status_word.
+ *   lse      [batch][heads][n_q] ln Σ_j exp(s·q_i·k_j), nullable: what the
+ *            backward needs beside out.
+ * dtype BSA_BF16, head_dim 64 or 128, any n_q, n_k >= 1 (BSA_ERR_UNSUPPORTED
+ * for another type or head_dim, or sizes past 32-bit row numbers).
+ * Products take bf16 operands (the softmax weights rounded to bf16 for the
+ * product with v), sums and softmax statistics are fp32; out is rounded once.
+ *
+ * `workspace` (device, >= bsa_cross_workspace_size bytes, 256-byte aligned;
+ * may be null where that size is 0) holds the parts of a key axis that is
+ * split when there are few query rows. Every call rewrites what it reads of
+ * it; calls that overlap on the GPU need workspaces of their own. status_word:
+ * nullable device uint32, OR-ed, read by bsa_check_status. Results do not
+ * depend on the order in which the GPU runs the parts.
+ */
+typedef struct {
+    int32_t batch;          /* B >= 1 */
+    int32_t heads;          /* query heads, a multiple of kv_heads */
+    int32_t kv_heads;       /* key heads >= 1 */
+    int32_t n_q;            /* query rows of a head */
+    int32_t n_k;            /* states of a batch entry (the buffer's, see key_len) */
+    int32_t head_dim;       /* 64 or 128 */
+    int32_t dtype;          /* BSA_BF16 */
+    float scale;            /* logit scale s; 0 means 1/sqrt(head_dim) */
+} bsa_cross_config;
+
+BSA_API bsa_status bsa_cross_workspace_size(const bsa_cross_config *cfg, size_t *bytes);
+BSA_API bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
+                                       const int32_t *key_len, void *out, float *lse, void *workspace,
+                                       size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream);
+
+/*
+ * Gradients of the same with respect to q, k and v for dout = dL/dout
+ * ([batch][heads][n_q][head_dim], bf16), given out and lse of the forward:
+ * dq like q, dk and dv like k (the sum over the query heads that share a key
+ * head; zero behind key_len). fp32 accumulation, rounded to bf16 once; no
+ * atomics, so every gradient is the same bit for bit from call to call.
+ * workspace, status_word: as for the forward, of bsa_cross_backward_workspace_size.
+ */
+BSA_API bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t *bytes);
+BSA_API bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void *q, const void *k,
+                                                const void *v, const int32_t *key_len, const void *out,
+                                                const float *lse, const void *dout, void *dq, void *dk, void *dv,
+                                                void *workspace, size_t workspace_bytes, uint32_t *status_word,
+                                                cudaStream_t stream);
+
+/*
+ * Attention of an ensemble whose members share a long prefix of keys (the
+ * analysis a forecast starts from) and have some of their own (a member's
+ * steps so far): every query row attends to the prefix of its group and to its
+ * own batch entry's states, in one softmax,
+ *   o_i = Σ_{j < prefix_len} p_ij v'_j + Σ_{j < own_len} p_ij v_j.
+ * The batch is `groups` ensembles of batch / groups consecutive members. The
+ * prefix is read once for the rows of all members of a group together.
+ *   q, out              [batch][heads][n_q][head_dim]
+ *   k_prefix, v_prefix  [groups][kv_heads][n_prefix][head_dim]
+ *   k_own, v_own        [batch][kv_heads][n_own][head_dim]
+ *   prefix_len [groups], own_len [batch]: int32, nullable, as key_len above
+ *     (0 allowed in either; a row with no keys at all gives zeros).
+ * Types, shapes, workspace and status_word as for bsa_cross_attention.
+ */
+typedef struct {
+    int32_t batch;          /* members of all groups together */
+    int32_t groups;         /* ensembles; batch is a multiple of groups */
+    int32_t heads;          /* query heads, a multiple of kv_heads */
+    int32_t kv_heads;
+    int32_t n_q;            /* query rows of a head and member */
+    int32_t n_prefix;       /* shared states of a group */
+    int32_t n_own;          /* own states of a member (the buffer's, see own_len) */
+    int32_t head_dim;       /* 64 or 128 */
+    int32_t dtype;          /* BSA_BF16 */
+    float scale;            /* logit scale s; 0 means 1/sqrt(head_dim) */
+} bsa_prefix_config;
+
+BSA_API bsa_status bsa_prefix_workspace_size(const bsa_prefix_config *cfg, size_t *bytes);
+BSA_API bsa_status bsa_prefix_attention(const bsa_prefix_config *cfg, const void *q, const void *k_prefix,
+                                        const void *v_prefix, const int32_t *prefix_len, const void *k_own,
+                                        const void *v_own, const int32_t *own_len, void *out, void *workspace,
+                                        size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream);
 
 /* Static, human-readable name of a status code. */
 BSA_API const char *bsa_status_string(bsa_status status);
