@@ -1,15 +1,22 @@
 // Shared declarations of the dense attention over states of another length
-// (cross attention, its backward, and attention over a shared prefix).
+// (cross attention, its backward, and attention over a shared prefix): the
+// problem, how a forward's work is cut into units and handed to CTAs, and the
+// launchers.
 #pragma once
 
 #include "bsa_internal.cuh"
 
 namespace bsa {
 
-// One set of keys for the rows of a forward pass. The rows of a slab are
-// (member, head of the key head's group, query) with `rows` = (heads /
-// kv_heads)·n_q rows a member, which [B][H][n_q][d] keeps contiguous; the
-// members of one set share its keys.
+struct DenseProblem {
+    int64_t batch, heads, kv_heads, n_q, d;
+    int64_t rows;           // (heads / kv_heads) * n_q: rows of a batch entry and key head
+    float scale;
+};
+
+// One set of keys for the rows of a forward pass. The rows of a batch entry
+// ("member") and key head are its `rows` = (heads / kv_heads)·n_q query rows,
+// which [B][H][n_q][d] keeps contiguous; the members of one set share its keys.
 struct KeySet {
     const void *k, *v;      // [sets][kv_heads][n][d] bf16
     const int32_t *len;     // [sets], nullable
@@ -18,16 +25,146 @@ struct KeySet {
     int64_t members;        // batch entries that share a set
 };
 
-struct DenseProblem {
-    int64_t batch, heads, kv_heads, n_q, d;
-    int64_t rows;           // (heads / kv_heads) * n_q: rows of a batch entry and key head
-    float scale;
+constexpr int kTile = 128;          // query rows and keys of a tile
+constexpr int kFewRows = 32;        // at most so many rows a set and key head: the "few rows" form
+constexpr int kCtas = 148;          // SMs of a B200: the work is cut for one CTA each
+
+// How the rows of one KeySet are cut. A unit is up to two tiles of 128 rows of
+// one set and key head (all its rows in the few-rows form); its steps are the
+// key tiles of the set's length, at least one.
+struct FwdSet {
+    const int32_t *len;
+    int64_t n, sets, members;
+    int32_t few;            // all rows of a set and key head fit kFewRows
+    int32_t bb;             // members in a tile when rows <= 128, else 0 (a tile holds 128 rows of one member)
+    int32_t tpm;            // bb == 0: tiles a member
+    int64_t tiles, pairs;   // tiles and units of a set and key head
+    int64_t upz;            // units of a set: kv_heads * pairs
 };
 
-// Launchers (return cudaGetLastError()). s1.k may be null: one set of keys.
-cudaError_t launch_dense_fwd(const DenseProblem &p, const void *q, const KeySet &s0, const KeySet &s1, void *out,
-                             float *lse, uint32_t *status, cudaStream_t stream);
+// A forward pass over one or two sets (set 0's units come first). `stream`: the
+// steps of all units, end to end, are dealt to `ctas` CTAs in equal shares, so
+// that a CTA begins and ends inside a unit; the parts of such a unit are joined
+// afterwards. Otherwise CTA c takes the whole units c, c + ctas, ...
+struct FwdPlan {
+    FwdSet s[2];
+    int32_t nsets, stream, ctas;
+    int64_t rows, kv_heads, batch;
+};
+
+// Row i of tile t of set z, key head hk: its index in [B][kv_heads][rows], or -1.
+__host__ __device__ inline int64_t plan_row(const FwdPlan &p, const FwdSet &s, int64_t z, int64_t hk, int64_t t, int i) {
+    int64_t member, r;
+    if (s.bb) {
+        const int64_t mi = i / (int)p.rows;
+        if (mi >= s.bb) return -1;
+        member = t * s.bb + mi;
+        r = i - mi * p.rows;
+    } else {
+        member = t / s.tpm;
+        r = (t - member * s.tpm) * kTile + i;
+    }
+    if (member >= s.members || r >= p.rows) return -1;
+    return ((z * s.members + member) * p.kv_heads + hk) * p.rows + r;
+}
+
+// Workspace of a forward pass, in floats. Parts: two slots a CTA (slot 1: a unit
+// that the CTA begins and leaves unfinished, slot 0: one that it takes over) of
+// 256 rows each, the normalised o and the row's log2-sum-exp. Whole (two sets
+// only): the same of units that one CTA finished, by set and row.
+struct FwdLayout {
+    size_t part_o, part_lse, whole_o, whole_lse, total;
+};
+FwdPlan make_fwd_plan(const DenseProblem &p, const KeySet *sets, int nsets);
+FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d);
+
+// Launchers (return cudaGetLastError()).
+cudaError_t launch_dense_fwd(const DenseProblem &p, const void *q, const KeySet *sets, int nsets, void *out, float *lse,
+                             float *workspace, uint32_t *status, cudaStream_t stream);
 cudaError_t launch_dense_bwd(const DenseProblem &p, const void *q, const KeySet &s, const void *out, const float *lse,
                              const void *dout, void *dq, void *dk, void *dv, uint32_t *status, cudaStream_t stream);
+
+#ifdef __CUDACC__
+// Keys of set z, clamped to the buffer; a length outside it is flagged in *status (nullable).
+__device__ __forceinline__ int set_len(const int32_t *len, int64_t z, int64_t n, uint32_t *status) {
+    if (!len) return (int)n;
+    const int x = __ldg(len + z);
+    if (x >= 0 && x <= n) return x;
+    if (status) atomicOr(status, kStatusBadIndex);
+    return x < 0 ? 0 : (int)n;
+}
+__device__ __forceinline__ int set_steps(const FwdSet &s, int64_t z) {
+    return max(1, (set_len(s.len, z, s.n, nullptr) + kTile - 1) / kTile);
+}
+// Warp-wide: the sum over sets z < z1 of their units' steps.
+__device__ __forceinline__ int64_t steps_before(const FwdSet &s, int64_t z1, int lane) {
+    if (!s.len) return z1 * s.upz * set_steps(s, 0);
+    int64_t sum = 0;
+    for (int64_t z = lane; z < z1; z += 32) sum += set_steps(s, z);
+    for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+    return sum * s.upz;
+}
+// Of `total` steps dealt to `ctas` CTAs: the first of CTA c, and the CTA that has step x.
+__device__ __forceinline__ int64_t cta_first(int64_t c, int64_t total, int ctas) { return c * total / ctas; }
+__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int ctas) {
+    return (int)(((x + 1) * ctas + total - 1) / total) - 1;
+}
+// Warp-wide: the set, unit and step at which step x of the whole pass lies.
+struct StepAt {
+    int set, t, steps;      // step within the unit, steps of the unit
+    int64_t z, uu;          // set, unit of the set
+};
+__device__ __forceinline__ StepAt step_at(const FwdPlan &p, int64_t x, int lane) {
+    StepAt r;
+    r.set = 0;
+    if (p.nsets == 2) {
+        const int64_t n0 = steps_before(p.s[0], p.s[0].sets, lane);
+        if (x >= n0) {
+            r.set = 1;
+            x -= n0;
+        }
+    }
+    const FwdSet &s = p.s[r.set];
+    if (!s.len) {
+        r.steps = set_steps(s, 0);
+        r.z = x / (s.upz * r.steps);
+        x -= r.z * s.upz * r.steps;
+    } else {
+        for (int64_t z0 = 0;; z0 += 32) {              // 32 sets at a time: an inclusive scan of their steps
+            const int64_t z = z0 + lane;
+            const int st = z < s.sets ? set_steps(s, z) : 0;
+            int64_t inc = st * s.upz;
+            for (int i = 1; i < 32; i <<= 1) {
+                const int64_t y = __shfl_up_sync(0xffffffffu, inc, i);
+                if (lane >= i) inc += y;
+            }
+            const unsigned after = __ballot_sync(0xffffffffu, x < inc);
+            if (after) {
+                const int l = __ffs(after) - 1;
+                const int64_t end = __shfl_sync(0xffffffffu, inc, l);
+                r.steps = __shfl_sync(0xffffffffu, st, l);
+                r.z = z0 + l;
+                x -= end - r.steps * s.upz;
+                break;
+            }
+            x -= __shfl_sync(0xffffffffu, inc, 31);
+            if (z0 + 32 >= s.sets) {                   // not reached for x below the total
+                r.z = s.sets - 1;
+                r.steps = 1;
+                x = 0;
+                break;
+            }
+        }
+    }
+    r.uu = x / r.steps;
+    r.t = (int)(x - r.uu * r.steps);
+    return r;
+}
+__device__ __forceinline__ int64_t total_steps(const FwdPlan &p, int lane) {
+    int64_t n = steps_before(p.s[0], p.s[0].sets, lane);
+    if (p.nsets == 2) n += steps_before(p.s[1], p.s[1].sets, lane);
+    return n;
+}
+#endif
 
 }  // namespace bsa

@@ -57,6 +57,21 @@ bsa_status check_workspace(const void *workspace, size_t have, size_t need) {
     return aligned(workspace, 256) ? BSA_OK : BSA_ERR_ALIGNMENT;
 }
 
+KeySet cross_set(const bsa_cross_config *c, const void *k, const void *v, const int32_t *len) {
+    return KeySet{k, v, len, c->n_k, c->batch, 1};
+}
+void prefix_sets(const bsa_prefix_config *c, const void *kp, const void *vp, const int32_t *plen, const void *ko,
+                 const void *vo, const int32_t *olen, KeySet *sets) {
+    sets[0] = KeySet{kp, vp, plen, c->n_prefix, c->groups, c->batch / c->groups};
+    sets[1] = KeySet{ko, vo, olen, c->n_own, c->batch, 1};
+}
+// With or without lengths alike: the largest of the two plans.
+size_t fwd_bytes(const DenseProblem &p, const KeySet *sets, int nsets) {
+    KeySet full[2] = {sets[0], sets[nsets - 1]};
+    full[0].len = full[1].len = nullptr;
+    return bsa::fwd_layout_of(bsa::make_fwd_plan(p, full, nsets), p.d).total * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -66,7 +81,8 @@ bsa_status bsa_cross_workspace_size(const bsa_cross_config *cfg, size_t *bytes) 
     const bsa_status st = make_cross(cfg, &p);
     if (st != BSA_OK) return st;
     if (!bytes) return BSA_ERR_INVALID_ARG;
-    *bytes = 0;
+    const KeySet s = cross_set(cfg, nullptr, nullptr, nullptr);
+    *bytes = fwd_bytes(p, &s, 1);
     return BSA_OK;
 }
 
@@ -78,13 +94,13 @@ bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const
     if (st != BSA_OK) return st;
     if (!q || !k || !v || !out) return BSA_ERR_INVALID_ARG;
     if (out == q || out == k || out == v) return BSA_ERR_INVALID_ARG;
-    const bsa_status ws = check_workspace(workspace, workspace_bytes, 0);
+    const KeySet s = cross_set(cfg, k, v, key_len);
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, fwd_bytes(p, &s, 1));
     if (ws != BSA_OK) return ws;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(key_len, 4) || !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
-    const KeySet s{k, v, key_len, cfg->n_k, p.batch, 1}, none{};
-    return from_cuda(bsa::launch_dense_fwd(p, q, s, none, out, lse, status_word, stream));
+    return from_cuda(bsa::launch_dense_fwd(p, q, &s, 1, out, lse, static_cast<float *>(workspace), status_word, stream));
 }
 
 bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t *bytes) {
@@ -128,7 +144,9 @@ bsa_status bsa_prefix_workspace_size(const bsa_prefix_config *cfg, size_t *bytes
     const bsa_status st = make_prefix(cfg, &p);
     if (st != BSA_OK) return st;
     if (!bytes) return BSA_ERR_INVALID_ARG;
-    *bytes = 0;
+    KeySet sets[2];
+    prefix_sets(cfg, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, sets);
+    *bytes = fwd_bytes(p, sets, 2);
     return BSA_OK;
 }
 
@@ -143,15 +161,16 @@ bsa_status bsa_prefix_attention(const bsa_prefix_config *cfg, const void *q, con
     for (const void *x : in)
         if (!x || x == out) return BSA_ERR_INVALID_ARG;
     if (!out) return BSA_ERR_INVALID_ARG;
-    const bsa_status ws = check_workspace(workspace, workspace_bytes, 0);
+    KeySet sets[2];
+    prefix_sets(cfg, k_prefix, v_prefix, prefix_len, k_own, v_own, own_len, sets);
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, fwd_bytes(p, sets, 2));
     if (ws != BSA_OK) return ws;
     for (const void *x : in)
         if (!aligned(x, 16)) return BSA_ERR_ALIGNMENT;
     if (!aligned(out, 16) || !aligned(prefix_len, 4) || !aligned(own_len, 4) || !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
-    const KeySet pre{k_prefix, v_prefix, prefix_len, cfg->n_prefix, cfg->groups, p.batch / cfg->groups};
-    const KeySet own{k_own, v_own, own_len, cfg->n_own, p.batch, 1};
-    return from_cuda(bsa::launch_dense_fwd(p, q, pre, own, out, nullptr, status_word, stream));
+    return from_cuda(
+        bsa::launch_dense_fwd(p, q, sets, 2, out, nullptr, static_cast<float *>(workspace), status_word, stream));
 }
 
 }  // extern "C"

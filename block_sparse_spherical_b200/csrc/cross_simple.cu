@@ -1,5 +1,5 @@
-// Dense attention over states of another length on the CUDA cores, the plain
-// way: one warp a query row (forward, dq) or a key row (dk, dv), lane j holding
+// Gradients of dense attention over states of another length on the CUDA cores,
+// the plain way: one warp a query row (dq) or a key row (dk, dv), lane j holding
 // the j-th of 32 keys (rows) for the scores and d/32 channels for the sums.
 #include <math_constants.h>
 
@@ -10,16 +10,6 @@ namespace {
 
 constexpr int kWarps = 4;
 
-__device__ __forceinline__ int clamped_len(const int32_t *len, int64_t i, int64_t n, uint32_t *status) {
-    if (!len) return (int)n;
-    const int64_t x = __ldg(len + i);
-    if (x < 0 || x > n) {
-        if (status) atomicOr(status, kStatusBadIndex);
-        return x < 0 ? 0 : (int)n;
-    }
-    return (int)x;
-}
-
 template <int D>
 __device__ __forceinline__ float dot_row(const float *a, const __nv_bfloat16 *b) {
     float s = 0.f;
@@ -29,49 +19,6 @@ __device__ __forceinline__ float dot_row(const float *a, const __nv_bfloat16 *b)
         s = fmaf(a[c + 1], x.y, s);
     }
     return s;
-}
-
-template <int D>
-__global__ void fwd_kernel(DenseProblem p, const __nv_bfloat16 *q, KeySet s0, KeySet s1, __nv_bfloat16 *out,
-                           float *lse, uint32_t *status) {
-    __shared__ float qs[kWarps][D];
-    const int w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t row = (int64_t)blockIdx.x * kWarps + w;
-    if (row >= p.batch * p.kv_heads * p.rows) return;
-    const int64_t slab = row / p.rows, b = slab / p.kv_heads, hk = slab % p.kv_heads;
-    for (int c = lane; c < D; c += 32) qs[w][c] = __bfloat162float(q[row * D + c]) * p.scale;
-    __syncwarp();
-    float m = -CUDART_INF_F, l = 0.f, o[D / 32];
-    for (int e = 0; e < D / 32; ++e) o[e] = 0.f;
-    for (int part = 0; part < 2; ++part) {
-        const KeySet &s = part ? s1 : s0;
-        if (!s.k) continue;
-        const int64_t set = b / s.members, base = (set * p.kv_heads + hk) * s.n;
-        const int len = clamped_len(s.len, set, s.n, status);
-        const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(s.k) + base * D;
-        const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(s.v) + base * D;
-        for (int j0 = 0; j0 < len; j0 += 32) {
-            const int j = j0 + lane;
-            const float x = j < len ? dot_row<D>(qs[w], k + (int64_t)j * D) : -CUDART_INF_F;
-            float mx = x;
-            for (int i = 16; i; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, i));
-            const float mn = fmaxf(m, mx), a = m == mn ? 1.f : expf(m - mn);
-            const float pr = j < len ? expf(x - mn) : 0.f;
-            l = l * a + pr;
-            m = mn;
-            for (int e = 0; e < D / 32; ++e) o[e] *= a;
-            const int cnt = min(32, len - j0);
-            for (int jj = 0; jj < cnt; ++jj) {
-                const float pj = __shfl_sync(~0u, pr, jj);
-                for (int e = 0; e < D / 32; ++e)
-                    o[e] = fmaf(pj, __bfloat162float(v[(int64_t)(j0 + jj) * D + lane + 32 * e]), o[e]);
-            }
-        }
-    }
-    for (int i = 16; i; i >>= 1) l += __shfl_xor_sync(~0u, l, i);
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : CUDART_NAN_F);
-    for (int e = 0; e < D / 32; ++e) out[row * D + lane + 32 * e] = __float2bfloat16_rn(o[e] * inv);
-    if (lse && lane == 0) lse[row] = l == 0.f ? -CUDART_INF_F : m + logf(l);
 }
 
 // dq of one row: dq = s Σ_j p_j (dp_j - D) k_j
@@ -93,7 +40,7 @@ __global__ void dq_kernel(DenseProblem p, const __nv_bfloat16 *q, KeySet s, cons
     }
     for (int i = 16; i; i >>= 1) dt += __shfl_xor_sync(~0u, dt, i);
     __syncwarp();
-    const int len = clamped_len(s.len, b, s.n, status);
+    const int len = set_len(s.len, b, s.n, status);
     const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(s.k) + slab * s.n * D;
     const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(s.v) + slab * s.n * D;
     const float ls = lse[row];
@@ -124,7 +71,7 @@ __global__ void dkv_kernel(DenseProblem p, const __nv_bfloat16 *q, KeySet s, con
     const int64_t row = (int64_t)blockIdx.x * kWarps + w;
     if (row >= p.batch * p.kv_heads * s.n) return;
     const int64_t slab = row / s.n, b = slab / p.kv_heads;
-    const int len = clamped_len(s.len, b, s.n, status);
+    const int len = set_len(s.len, b, s.n, status);
     float ak[D / 32], av[D / 32];
     for (int e = 0; e < D / 32; ++e) ak[e] = av[e] = 0.f;
     if (row % s.n < len) {
@@ -165,15 +112,6 @@ using bf = __nv_bfloat16;
 unsigned ctas(int64_t rows) { return (unsigned)((rows + kWarps - 1) / kWarps); }
 
 }  // namespace
-
-cudaError_t launch_dense_fwd(const DenseProblem &p, const void *q, const KeySet &s0, const KeySet &s1, void *out,
-                             float *lse, uint32_t *status, cudaStream_t stream) {
-    const int64_t rows = p.batch * p.kv_heads * p.rows;
-    auto kern = p.d == 64 ? fwd_kernel<64> : fwd_kernel<128>;
-    kern<<<ctas(rows), 32 * kWarps, 0, stream>>>(p, static_cast<const bf *>(q), s0, s1, static_cast<bf *>(out), lse,
-                                                 status);
-    return cudaGetLastError();
-}
 
 cudaError_t launch_dense_bwd(const DenseProblem &p, const void *q, const KeySet &s, const void *out, const float *lse,
                              const void *dout, void *dq, void *dk, void *dv, uint32_t *status, cudaStream_t stream) {
