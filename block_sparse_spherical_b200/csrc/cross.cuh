@@ -40,6 +40,8 @@ struct FwdSet {
     int32_t tpm;            // bb == 0: tiles a member
     int64_t tiles, pairs;   // tiles and units of a set and key head
     int64_t upz;            // units of a set: kv_heads * pairs
+    int32_t fixed;          // > 0 (key-major backward): a unit is a key tile and has so many steps, its
+                            // query tiles; upz is then kv_heads * fixed, so that a set has upz steps a key tile
 };
 
 // A forward pass over one or two sets (set 0's units come first). `stream`: the
@@ -81,8 +83,10 @@ FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d);
 // Launchers (return cudaGetLastError()).
 cudaError_t launch_dense_fwd(const DenseProblem &p, const void *q, const KeySet *sets, int nsets, void *out, float *lse,
                              float *workspace, uint32_t *status, cudaStream_t stream);
+size_t dense_bwd_floats(const DenseProblem &p, const KeySet &s);   // workspace of a backward pass
 cudaError_t launch_dense_bwd(const DenseProblem &p, const void *q, const KeySet &s, const void *out, const float *lse,
-                             const void *dout, void *dq, void *dk, void *dv, uint32_t *status, cudaStream_t stream);
+                             const void *dout, void *dq, void *dk, void *dv, float *workspace, uint32_t *status,
+                             cudaStream_t stream);
 
 #ifdef __CUDACC__
 // Keys of set z, clamped to the buffer; a length outside it is flagged in *status (nullable).
@@ -156,6 +160,7 @@ __device__ __forceinline__ StepAt step_at(const FwdPlan &p, int64_t x, int lane)
             }
         }
     }
+    if (s.fixed) r.steps = s.fixed;
     r.uu = x / r.steps;
     r.t = (int)(x - r.uu * r.steps);
     return r;

@@ -72,6 +72,11 @@ size_t fwd_bytes(const DenseProblem &p, const KeySet *sets, int nsets) {
     return bsa::fwd_layout_of(bsa::make_fwd_plan(p, full, nsets), p.d).total * sizeof(float);
 }
 
+size_t bwd_bytes(const DenseProblem &p, KeySet s) {
+    s.len = nullptr;
+    return bsa::dense_bwd_floats(p, s) * sizeof(float);
+}
+
 }  // namespace
 
 extern "C" {
@@ -108,7 +113,7 @@ bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t
     const bsa_status st = make_cross(cfg, &p);
     if (st != BSA_OK) return st;
     if (!bytes) return BSA_ERR_INVALID_ARG;
-    *bytes = 0;
+    *bytes = bwd_bytes(p, cross_set(cfg, nullptr, nullptr, nullptr));
     return BSA_OK;
 }
 
@@ -128,15 +133,16 @@ bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void 
         for (const void *x : in)
             if (x == grads[i]) return BSA_ERR_INVALID_ARG;
     }
-    const bsa_status ws = check_workspace(workspace, workspace_bytes, 0);
+    const KeySet s = cross_set(cfg, k, v, key_len);
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, bwd_bytes(p, s));
     if (ws != BSA_OK) return ws;
     for (int i = 0; i < 5; ++i)
         if (!aligned(in[i], 16)) return BSA_ERR_ALIGNMENT;
     if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4) || !aligned(key_len, 4) ||
         !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
-    const KeySet s{k, v, key_len, cfg->n_k, p.batch, 1};
-    return from_cuda(bsa::launch_dense_bwd(p, q, s, out, lse, dout, dq, dk, dv, status_word, stream));
+    return from_cuda(bsa::launch_dense_bwd(p, q, s, out, lse, dout, dq, dk, dv, static_cast<float *>(workspace), status_word,
+                                           stream));
 }
 
 bsa_status bsa_prefix_workspace_size(const bsa_prefix_config *cfg, size_t *bytes) {

@@ -37,7 +37,7 @@
 #include <math_constants.h>
 
 #include "cross.cuh"
-#include "tc_common.cuh"
+#include "cross_tc.cuh"
 
 namespace bsa {
 namespace {
@@ -165,22 +165,6 @@ __device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c,
 // D = 64: K0 K1 V0 K2 V1 ... (S of the next step goes before this one's P·V), else K0 V0 K1 V1 ...
 template <int D> __device__ __forceinline__ bool looks_ahead(bool few) { return D == 64 && !few; }
 
-__device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2,
-                                            int c3) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
-        : "memory");
-}
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int c0, int c1, int c2) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
 template <int D>
 __device__ void copy_role(const FwdParams &p, const Maps &maps, Shared<D> &sh, int lane) {
     using C = Cfg<D>;
@@ -269,24 +253,9 @@ __device__ void copy_role(const FwdParams &p, const Maps &maps, Shared<D> &sh, i
     }
 }
 
-// D (TMEM) (+)= A·B with A (K-major bf16 pairs, the lanes of D) read from tensor memory.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 template <int D> __device__ __forceinline__ uint32_t col_s(int pl) { return 128u * pl; }
 template <int D> __device__ __forceinline__ uint32_t col_p(int pl) { return D == 64 ? 256u + 64u * pl : 128u * pl; }
 template <int D> __device__ __forceinline__ uint32_t col_o(int pl) { return D == 64 ? 384u + 64u * pl : 256u + 128u * pl; }
-
-constexpr uint32_t idesc_of(int n, bool b_mn) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
 
 template <int D>
 __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int pl, int lane) {
@@ -381,16 +350,6 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
     if (leader) commit(&sh.drain[pl]);
     __syncwarp();
     drain_bar(&sh.drain[pl], 0);
-}
-
-// 32 lanes x 16 columns: thread t of the warp writes TMEM lane (base + t).
-__device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t *u) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-        "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "r"(u[8]),
-        "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
-        : "memory");
 }
 
 __device__ __forceinline__ float max32(const float *s) {
@@ -845,16 +804,6 @@ template <int D> __global__ void __launch_bounds__(256) join_two_kernel(const __
 }
 
 // ---------------------------------------------------------------- host
-
-bool make_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
-              const cuuint32_t *box) {
-    auto fn = encode_tiled_fn();
-    if (!fn) return false;
-    const cuuint32_t one[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 template <int D>
 cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet *sets, FwdParams &p, cudaStream_t stream) {
