@@ -44,41 +44,49 @@ struct FwdSet {
                             // query tiles; upz is then kv_heads * fixed, so that a set has upz steps a key tile
 };
 
-// A forward pass over one or two sets (set 0's units come first). `stream`: the
-// steps of all units, end to end, are dealt to `ctas` CTAs in equal shares, so
-// that a CTA begins and ends inside a unit; the parts of such a unit are joined
+// A pass over one KeySet. `stream`: the steps of all units, end to end, are dealt to `ctas` CTAs in
+// equal shares, so that a CTA begins and ends inside a unit; the parts of such a unit are joined
 // afterwards. Otherwise CTA c takes the whole units c, c + ctas, ...
 struct FwdPlan {
-    FwdSet s[2];
-    int32_t nsets, stream, ctas;
+    FwdSet s;
+    int32_t stream, ctas;
     int64_t rows, kv_heads, batch;
 };
 
-// Row i of tile t of set z, key head hk: its index in [B][kv_heads][rows], or -1.
-__host__ __device__ inline int64_t plan_row(const FwdPlan &p, const FwdSet &s, int64_t z, int64_t hk, int64_t t, int i) {
-    int64_t member, r;
+// Row i of tile t of set z, key head hk: its index in [B][kv_heads][rows], or -1. (32-bit divisions: a
+// tile number of rows that fit a GPU is far below 2^31.)
+__host__ __device__ inline int64_t plan_row(const FwdPlan &p, int64_t z, int64_t hk, int64_t t, int i) {
+    const FwdSet &s = p.s;
+    const uint32_t rows = (uint32_t)p.rows;
+    uint32_t member, r;
     if (s.bb) {
-        const int64_t mi = i / (int)p.rows;
-        if (mi >= s.bb) return -1;
-        member = t * s.bb + mi;
-        r = i - mi * p.rows;
+        const uint32_t mi = (uint32_t)i / rows;
+        if (mi >= (uint32_t)s.bb) return -1;
+        member = (uint32_t)t * s.bb + mi;
+        r = i - mi * rows;
     } else {
-        member = t / s.tpm;
-        r = (t - member * s.tpm) * kTile + i;
+        member = (uint32_t)t / (uint32_t)s.tpm;
+        r = ((uint32_t)t - member * s.tpm) * kTile + i;
     }
-    if (member >= s.members || r >= p.rows) return -1;
+    if (member >= (uint32_t)s.members || r >= rows) return -1;
     return ((z * s.members + member) * p.kv_heads + hk) * p.rows + r;
 }
 
-// Workspace of a forward pass, in floats. Parts: two slots a CTA (slot 1: a unit
-// that the CTA begins and leaves unfinished, slot 0: one that it takes over) of
-// 256 rows each, the normalised o and the row's log2-sum-exp. Whole (two sets
-// only): the same of units that one CTA finished, by set and row.
-struct FwdLayout {
-    size_t part_o, part_lse, whole_o, whole_lse, total;
+// A unit that is cut, as its first CTA c leaves it for the join: its parts are that CTA's slot 1 and
+// slot 0 of the CTAs up to `last`. last < 0: CTA c leaves none.
+struct Cut {
+    int32_t z, hk, tile, last;      // tile: pair of tiles (key-major backward: key tile)
 };
-FwdPlan make_fwd_plan(const DenseProblem &p, const KeySet *sets, int nsets);
-FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d);
+
+// Workspace of a forward pass over a set, in floats. Parts: two slots a CTA (slot 1: a unit that the CTA
+// begins and leaves unfinished, slot 0: one that it takes over) of 256 rows each, the normalised o
+// and the row's log2-sum-exp. With two sets also: whole, the same of units that one CTA finished, by
+// row, and of every unit its first and last CTA.
+struct FwdLayout {
+    size_t part_o, part_lse, cuts, whole_o, whole_lse, spans, total;
+};
+FwdPlan make_fwd_plan(const DenseProblem &p, const KeySet &set);
+FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d, bool two_sets);
 
 // Launchers (return cudaGetLastError()).
 cudaError_t launch_dense_fwd(const DenseProblem &p, const void *q, const KeySet *sets, int nsets, void *out, float *lse,
@@ -108,27 +116,23 @@ __device__ __forceinline__ int64_t steps_before(const FwdSet &s, int64_t z1, int
     for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
     return sum * s.upz;
 }
-// Of `total` steps dealt to `ctas` CTAs: the first of CTA c, and the CTA that has step x.
-__device__ __forceinline__ int64_t cta_first(int64_t c, int64_t total, int ctas) { return c * total / ctas; }
-__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int ctas) {
-    return (int)(((x + 1) * ctas + total - 1) / total) - 1;
+// Of `total` steps dealt to min(ctas, total) CTAs: the first of CTA c, and the CTA that has step x.
+__device__ __forceinline__ int64_t cta_first(int64_t c, int64_t total, int ctas) {
+    const int64_t n = min((int64_t)ctas, total);
+    return min(c, n) * total / n;
 }
-// Warp-wide: the set, unit and step at which step x of the whole pass lies.
+__device__ __forceinline__ int cta_of(int64_t x, int64_t total, int ctas) {
+    const int64_t n = min((int64_t)ctas, total);
+    return (int)(((x + 1) * n + total - 1) / total) - 1;
+}
+// Warp-wide: the unit and step at which step x of the whole pass lies.
 struct StepAt {
-    int set, t, steps;      // step within the unit, steps of the unit
+    int t, steps;           // step within the unit, steps of the unit
     int64_t z, uu;          // set, unit of the set
 };
 __device__ __forceinline__ StepAt step_at(const FwdPlan &p, int64_t x, int lane) {
     StepAt r;
-    r.set = 0;
-    if (p.nsets == 2) {
-        const int64_t n0 = steps_before(p.s[0], p.s[0].sets, lane);
-        if (x >= n0) {
-            r.set = 1;
-            x -= n0;
-        }
-    }
-    const FwdSet &s = p.s[r.set];
+    const FwdSet &s = p.s;
     if (!s.len) {
         r.steps = set_steps(s, 0);
         r.z = x / (s.upz * r.steps);
@@ -165,11 +169,7 @@ __device__ __forceinline__ StepAt step_at(const FwdPlan &p, int64_t x, int lane)
     r.t = (int)(x - r.uu * r.steps);
     return r;
 }
-__device__ __forceinline__ int64_t total_steps(const FwdPlan &p, int lane) {
-    int64_t n = steps_before(p.s[0], p.s[0].sets, lane);
-    if (p.nsets == 2) n += steps_before(p.s[1], p.s[1].sets, lane);
-    return n;
-}
+__device__ __forceinline__ int64_t total_steps(const FwdPlan &p, int lane) { return steps_before(p.s, p.s.sets, lane); }
 #endif
 
 }  // namespace bsa

@@ -65,13 +65,16 @@ void prefix_sets(const bsa_prefix_config *c, const void *kp, const void *vp, con
     sets[0] = KeySet{kp, vp, plen, c->n_prefix, c->groups, c->batch / c->groups};
     sets[1] = KeySet{ko, vo, olen, c->n_own, c->batch, 1};
 }
-// With or without lengths alike: the largest of the two plans.
+// With or without lengths alike: a pass without lengths needs at least what one with lengths does.
 size_t fwd_bytes(const DenseProblem &p, const KeySet *sets, int nsets) {
-    KeySet full[2] = {sets[0], sets[nsets - 1]};
-    full[0].len = full[1].len = nullptr;
-    return bsa::fwd_layout_of(bsa::make_fwd_plan(p, full, nsets), p.d).total * sizeof(float);
+    size_t floats = 0;
+    for (int k = 0; k < nsets; ++k) {
+        KeySet full = sets[k];
+        full.len = nullptr;
+        floats += bsa::fwd_layout_of(bsa::make_fwd_plan(p, full), p.d, nsets == 2).total;
+    }
+    return floats * sizeof(float);
 }
-
 size_t bwd_bytes(const DenseProblem &p, KeySet s) {
     s.len = nullptr;
     return bsa::dense_bwd_floats(p, s) * sizeof(float);

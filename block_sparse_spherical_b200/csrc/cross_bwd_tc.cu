@@ -45,7 +45,7 @@ constexpr int kSub = 64;                    // query rows (key-major) or keys (q
 constexpr int kStat = 2 * kSub;             // floats of a query tile's statistics: lse·log2 e, then D
 
 struct BwdParams {
-    FwdPlan plan;           // key-major: s[0].fixed query tiles a unit; query-major: as a forward's
+    FwdPlan plan;           // key-major: s.fixed query tiles a unit; query-major: as a forward's
     const float *stat;      // [slabs][query tiles of 64][2][64]
     int64_t qtiles;         // query tiles of 64 rows a slab
     __nv_bfloat16 *dq, *dk, *dv;
@@ -94,7 +94,7 @@ __global__ void __launch_bounds__(256) bwd_stat_kernel(const __grid_constant__ B
             s[kSub] = x == CUDART_INF_F ? 0.f : d;
         }
     }
-    const FwdSet &s = p.plan.s[0];
+    const FwdSet &s = p.plan.s;
     if (!s.len) return;
     for (int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L; i < slabs * s.n; i += step) {
         const int64_t slab = i / s.n;
@@ -144,7 +144,7 @@ template <int D> __device__ __forceinline__ KeyWalk key_begin(const BwdParams &p
     return w;
 }
 __device__ __forceinline__ bool key_next(const BwdParams &p, KeyWalk &w, KeyChunk &c, uint32_t *status) {
-    const FwdSet &s = p.plan.s[0];
+    const FwdSet &s = p.plan.s;
     const int64_t hk_n = p.plan.kv_heads;
     int64_t hk;
     int len;
@@ -187,9 +187,9 @@ template <int D>
 __device__ void key_copy_role(const BwdParams &p, const BwdMaps &maps, KeyShared<D> &sh, int lane) {
     using C = KeyCfg<D>;
     volatile int *abort_flag = &sh.abort_flag;
-    const bool leader = lane == 0;
+    const bool leader = elect_one();    // issues; the whole warp runs the loop
     auto wait_w = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     uint32_t u = 0, g = 0;
     bool ok = true;
@@ -243,9 +243,9 @@ template <int D>
 __device__ void key_score_role(const BwdParams &p, KeyShared<D> &sh, uint32_t tmem, int lane) {
     using C = KeyCfg<D>;
     volatile int *abort_flag = &sh.abort_flag;
-    const bool leader = lane == 0;
+    const bool leader = elect_one();    // issues; the whole warp runs the loop
     auto wait_w = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     const uint64_t dk0 = desc_kmajor_sw128(sh.k[0]), dv0 = desc_kmajor_sw128(sh.v[0]);
     const uint64_t dq0 = desc_kmajor_sw128(sh.q[0]), do0 = desc_kmajor_sw128(sh.o[0]);
@@ -296,9 +296,9 @@ template <int D>
 __device__ void key_grad_role(const BwdParams &p, KeyShared<D> &sh, uint32_t tmem, int lane) {
     using C = KeyCfg<D>;
     volatile int *abort_flag = &sh.abort_flag;
-    const bool leader = lane == 0;
+    const bool leader = elect_one();    // issues; the whole warp runs the loop
     auto wait_w = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     const uint64_t dq0 = desc_mnmajor_sw128(sh.q[0], kSub * 128), do0 = desc_mnmajor_sw128(sh.o[0], kSub * 128);
     uint32_t u = 0, g = 0;
@@ -354,7 +354,7 @@ __device__ void key_softmax_role(const BwdParams &p, KeyShared<D> &sh, uint32_t 
     using C = KeyCfg<D>;
     volatile int *abort_flag = &sh.abort_flag;
     auto wait_all = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     const uint32_t tw = tmem + ((uint32_t)(32 * wq) << 16);
     const int row = 32 * wq + lane;          // this thread's key of the tile
@@ -405,7 +405,7 @@ __device__ void key_softmax_role(const BwdParams &p, KeyShared<D> &sh, uint32_t 
             }
             if constexpr (D == 64) {
                 fence_before();
-                mbar_arrive(&sh.s_free[grp]);
+                warp_arrive(&sh.s_free[grp], lane);
             }
             if (!counts) {
 #pragma unroll
@@ -418,14 +418,14 @@ __device__ void key_softmax_role(const BwdParams &p, KeyShared<D> &sh, uint32_t 
             tmem_st32(tw + key_ds<D>(grp), reinterpret_cast<const float *>(ds));
             tmem_wait_st();
             fence_before();
-            mbar_arrive(&sh.p_full[grp]);
+            warp_arrive(&sh.p_full[grp], lane);
         }
         if (!ok || !(ok = wait_all(&sh.acc_full, u & 1))) break;
         ++u;
         fence_after();
         // group 0 stores dv, group 1 dk
         const uint32_t col = grp ? kColDk<D> : kColDv<D>;
-        const int64_t at = c.slab * p.plan.s[0].n + (int64_t)c.tile * kTile + row;
+        const int64_t at = c.slab * p.plan.s.n + (int64_t)c.tile * kTile + row;
         __nv_bfloat16 *d16 = c.slot >= 0 ? nullptr : (grp ? p.dk : p.dv) + at * D;
         float *d32 = p.part + (((2 * (int64_t)blockIdx.x + max(c.slot, 0)) * kTile + row) * 2 + grp) * D;
 #pragma unroll 1
@@ -436,7 +436,7 @@ __device__ void key_softmax_role(const BwdParams &p, KeyShared<D> &sh, uint32_t 
             if (counts) grad32(d16 ? d16 + 32 * cc : nullptr, d32 + 32 * cc, x, grp ? p.scale : 1.f);
         }
         fence_before();
-        mbar_arrive(&sh.acc_free);
+        warp_arrive(&sh.acc_free, lane);
     }
 }
 
@@ -445,15 +445,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_key_kernel(const __grid_const
                                                               const __grid_constant__ BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     KeyShared<D> &sh = *reinterpret_cast<KeyShared<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         sh.abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.kv_full[i], 1);
             mbar_init(&sh.kv_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_free[i], 128);
-            mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.s_free[i], 4);
+            mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.g_done[i], 1);
             mbar_init(&sh.drain[i], 1);
         }
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_key_kernel(const __grid_const
             mbar_init(&sh.st_empty[i], 2);
         }
         mbar_init(&sh.acc_full, 1);
-        mbar_init(&sh.acc_free, 256);
+        mbar_init(&sh.acc_free, 8);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -543,7 +543,7 @@ template <int D> __device__ __forceinline__ QryWalk qry_begin(const BwdParams &p
     return w;
 }
 __device__ __forceinline__ bool qry_next(const BwdParams &p, QryWalk &w, QryChunk &c, uint32_t *status) {
-    const FwdSet &s = p.plan.s[0];
+    const FwdSet &s = p.plan.s;
     int64_t z, uu;
     int t0, n;
     if (p.plan.stream) {
@@ -586,11 +586,11 @@ template <int D>
 __device__ void qry_copy_role(const BwdParams &p, const BwdMaps &maps, QryShared<D> &sh, int lane) {
     using C = QryCfg<D>;
     volatile int *abort_flag = &sh.abort_flag;
-    const bool leader = lane == 0;
+    const bool leader = elect_one();    // issues; the whole warp runs the loop
     auto wait_w = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
-    const FwdSet &s = p.plan.s[0];
+    const FwdSet &s = p.plan.s;
     uint32_t nq[2] = {0, 0}, g = 0, ntail = 0;
     bool ok = true;
     QryChunk c;
@@ -662,9 +662,9 @@ template <int D>
 __device__ void qry_mma_role(const BwdParams &p, QryShared<D> &sh, uint32_t tmem, int pl, int lane) {
     using C = QryCfg<D>;
     volatile int *abort_flag = &sh.abort_flag;
-    const bool leader = lane == 0;
+    const bool leader = elect_one();    // issues; the whole warp runs the loop
     auto wait_w = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     const uint32_t tp = tmem + 256u * pl;
     const uint64_t dq = desc_kmajor_sw128(sh.q[pl]), dO = desc_kmajor_sw128(sh.o[pl]);
@@ -716,7 +716,7 @@ __device__ void qry_mma_role(const BwdParams &p, QryShared<D> &sh, uint32_t tmem
     QryWalk w = qry_begin<D>(p, sh);
     while (ok && qry_next(p, w, c, nullptr)) {
         if (c.nt <= 0) continue;
-        if (2 * c.pair + pl >= p.plan.s[0].tiles) {
+        if (2 * c.pair + pl >= p.plan.s.tiles) {
             for (int t = 0; t < c.nt && ok; ++t) {     // released once there
                 const int st = (pos + t) % C::STAGES;
                 ok = wait_w(&sh.st_full[st], ((pos + t) / C::STAGES) & 1);
@@ -749,12 +749,12 @@ template <int D>
 __device__ void qry_softmax_role(const BwdParams &p, QryShared<D> &sh, uint32_t tmem, int pl, int wq, int lane) {
     volatile int *abort_flag = &sh.abort_flag;
     auto wait_all = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     const uint32_t tw = tmem + 256u * pl + ((uint32_t)(32 * wq) << 16);
     const int i = 32 * wq + lane;            // this thread's row of the tile
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
-    const FwdSet &s = p.plan.s[0];
+    const FwdSet &s = p.plan.s;
     uint32_t g = 0, nu = 0;
     bool ok = true;
     QryChunk c;
@@ -799,11 +799,11 @@ __device__ void qry_softmax_role(const BwdParams &p, QryShared<D> &sh, uint32_t 
                 for (int e = 0; e < 16; ++e) ds[16 * h + e] = pack_bf16x2(e2[e].x, e2[e].y);
             }
             fence_before();
-            if constexpr (D == 64) mbar_arrive(&sh.s_free[pl]);
+            if constexpr (D == 64) warp_arrive(&sh.s_free[pl], lane);
             tmem_st32(tw + qry_s<D>(g), reinterpret_cast<const float *>(ds));
             tmem_wait_st();
             fence_before();
-            mbar_arrive(&sh.p_full[pl]);
+            warp_arrive(&sh.p_full[pl], lane);
         }
         if (!ok) break;
         if (c.nt > 0) {
@@ -834,15 +834,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_qry_kernel(const __grid_const
                                                               const __grid_constant__ BwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     QryShared<D> &sh = *reinterpret_cast<QryShared<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         sh.abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_empty[i], 1);
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_free[i], 128);
-            mbar_init(&sh.p_full[i], 128);
+            mbar_init(&sh.s_free[i], 4);
+            mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.acc_full[i], 1);
             mbar_init(&sh.drain[i], 1);
         }
@@ -903,7 +903,7 @@ __device__ __forceinline__ void add_parts(const BwdParams &p, int c, int rowbloc
     const int64_t a = x - at.t;
     if (cta_of(a, total, p.plan.ctas) != c - 1) return;
     const int cb = cta_of(a + at.steps - 1, total, p.plan.ctas);
-    const FwdSet &s = p.plan.s[0];
+    const FwdSet &s = p.plan.s;
     constexpr int ROWS = KEY ? kTile : 2 * kTile, W = KEY ? 2 * D : D, E = W / 32;   // floats a row, a lane
     const int i = 8 * rowblock + warp;
     int64_t row;
@@ -921,7 +921,6 @@ __device__ __forceinline__ void add_parts(const BwdParams &p, int c, int rowbloc
 #pragma unroll
     for (int e = 0; e < E; ++e) sum[e] = 0.f;
     for (int k = c - 1; k <= cb; ++k) {
-        if (total < p.plan.ctas && cta_first(k, total, p.plan.ctas) == cta_first(k + 1, total, p.plan.ctas)) continue;
         const float2 *src = reinterpret_cast<const float2 *>(p.part + ((2 * (int64_t)k + (k == c - 1)) * ROWS + i) * W);
 #pragma unroll
         for (int e = 0; e < E / 2; ++e) {
@@ -941,7 +940,7 @@ __device__ __forceinline__ void add_parts(const BwdParams &p, int c, int rowbloc
 template <int D>
 __global__ void __launch_bounds__(256) bwd_join_kernel(const __grid_constant__ BwdParams key, const __grid_constant__ BwdParams qry,
                                                        int key_blocks) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     int b = blockIdx.x;
     if (b < key_blocks) {
         add_parts<D, true>(key, b / (kTile / 8) + 1, b % (kTile / 8), warp, lane);
@@ -961,14 +960,14 @@ struct BwdPlans {
 
 BwdPlans make_plans(const DenseProblem &p, const KeySet &ks) {
     BwdPlans r;
-    r.qry = make_fwd_plan(p, &ks, 1);
-    FwdSet &q = r.qry.s[0];
+    r.qry = make_fwd_plan(p, ks);
+    FwdSet &q = r.qry.s;
     q.few = 0;
     q.bb = 0;
     q.tpm = (int32_t)((p.rows + kTile - 1) / kTile);
     r.qtiles = (p.rows + kSub - 1) / kSub;
     r.key = r.qry;
-    FwdSet &s = r.key.s[0];
+    FwdSet &s = r.key.s;
     s.fixed = (int32_t)r.qtiles;
     s.upz = p.kv_heads * r.qtiles;
     const int64_t kt = (ks.n + kTile - 1) / kTile, units = ks.sets * p.kv_heads * kt;

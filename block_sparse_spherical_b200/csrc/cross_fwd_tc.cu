@@ -13,28 +13,36 @@
 //   warp 0       copies (TMA, 128-byte swizzle): Q of a unit, then K and V tiles
 //                through one ring that both pipelines read
 //   warps 1, 2   the MMA warp of pipeline 0 and of pipeline 1
-//   warp 3       finds the CTA's first unit
+//   warp 3       finds the CTA's units and hands them out
 //   warps 4-7, 8-11  softmax and epilogue of pipeline 0 and of pipeline 1
 // Many rows: the pipelines hold two tiles of 128 rows of one unit and both take
-// every key tile, so K and V are read once for 256 rows, and one pipeline's
-// products run beside the other's softmax. Few rows (at most 32: a decoding step's
-// query heads, or an ensemble's members together): both hold the same rows, four
-// times over in the four 32-lane quarters of tensor memory, and take alternate key
-// tiles; warp w of a pipeline does the softmax of its tile's keys 32w..32w+31 only
-// (P is zero elsewhere in its lanes). So the exponentials of a tile are spread over
-// all threads although there are few rows, and the eight partial rows are merged by
-// their maxima and sums at the unit's end.
+// every key tile, so K and V are read once for 256 rows. A thread owns a row. A step
+// is half a key tile, and S has two buffers: the MMA warp issues S(0) S(1) PV(0) S(2)
+// PV(1) ..., so that the products of one step, from the arrival of its P to the next S
+// (about 1,000 clocks), run beside the softmax of the other. P(u) takes the place of
+// S(u), which S(u+2) overwrites behind P·V(u). With steps of a whole tile, P had
+// to wait for the P·V before it and every step paid that chain (2.09 us for 256 rows
+// and 128 keys at D = 64, where the exponentials alone need 1.08); two threads a row did
+// not help, the chain was the same.
+// Few rows (at most 32: a decoding step's query heads, or an ensemble's members
+// together): both pipelines hold the same rows, four times over in the four 32-lane
+// quarters of tensor memory, and take alternate key tiles; warp w of a pipeline does
+// the softmax of its tile's keys 32w..32w+31 only (P is zero elsewhere in its lanes).
+// So the exponentials of a tile are spread over four warps although there are few
+// rows, and the eight partial rows are merged by their maxima and sums at the end.
 //
-// Tensor memory (512 columns): D = 64: S0 S1 (128 each), P0 P1 (64 each), O0 O1 (64
-// each); S of the next step is formed while this one's softmax runs. D = 128: S0 S1,
-// O0 O1 (128 each); P takes the first 64 columns of its S, and S of the next step
-// follows P·V in the issue order of its pipeline.
+// Tensor memory (512 columns): many rows: S buffer b of pipeline p 128p + 64b.., O 256 + D·p..
+// Few rows: D = 64: S0 S1 (128 each), P0 P1 (64 each), O0 O1 (64 each); S of the next tile is
+// formed while this one's softmax runs. D = 128: S0 S1, O0 O1 (128 each); P takes the first
+// 64 columns of its S, and S of the next tile follows P·V.
 //
 // Keys behind a length: scores are replaced before the maximum (whatever K holds),
 // and the copy warp zeroes those rows of V in shared memory, since 0·NaN is NaN.
 //
 // Every wait on an mbarrier is bounded (2 s), as in the block-sparse kernel.
 #include <math_constants.h>
+
+#include <type_traits>
 
 #include "cross.cuh"
 #include "cross_tc.cuh"
@@ -48,6 +56,13 @@ constexpr int NTHREADS = 384;
 constexpr int kCtrlRegs = 72, kSoftRegs = 216;
 constexpr int kRegsNeeded = 128 * kCtrlRegs + 256 * kSoftRegs;
 static_assert(kRegsNeeded <= 65536, "register split");
+constexpr int kReaders = 11;                // warps that read a chunk: copy, 2 MMA, 8 softmax
+constexpr int kSub = 64;                    // keys of a step when there are many rows
+// Of 16 pairs of exponentials, how many take the polynomial on the FMA pipe. D = 64 is bound by the
+// exponentials (a step of 256 rows and 128 keys: none 1.86 us, 4 of 16 1.69, 6 of 16 1.75), D = 128
+// by the chain of its products (none 2.33 us, 4 of 16 2.44).
+template <int D> constexpr int kPoly = D == 64 ? 4 : 0;
+constexpr int GRP = 8;                      // pairs in a phase
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -59,15 +74,31 @@ template <int D> struct Cfg {
     static constexpr int MSTRIDE = D + 4;              // floats, padded against bank conflicts
 };
 
+// What a CTA does next: key tiles [t0, t0 + nt) of a unit; nt 0: a set without keys, -1: nothing more.
+// Warp 3 finds the chunks and hands them to the other warps through shared memory.
+struct Chunk {
+    int nt, t0, rel;        // rel: the set's keys from key tile t0 on
+    int slot;               // -1: the whole unit
+    int alone;              // many rows: the second pipeline has no tile
+    int64_t z, hk, pair;
+};
+struct Walk {
+    int t, steps;
+    int64_t z, uu, left;    // stream: steps left; whole: the unit's index
+    int64_t at, total;      // stream: the next step, all steps
+};
+constexpr int kChunks = 4;
+
 template <int D> struct alignas(1024) Shared {
     uint8_t q[2][Cfg<D>::TILE];
     uint8_t kv[Cfg<D>::STAGES][Cfg<D>::TILE];
     float merge[8][Cfg<D>::MROWS][Cfg<D>::MSTRIDE];
     float ml[2][8][32];                                // few rows: (m, l) of each partial row
     uint64_t q_full[2], q_empty[2], kv_full[Cfg<D>::STAGES], kv_empty[Cfg<D>::STAGES], tail;
-    uint64_t s_full[2], s_free[2], p_full[2], o_done[2], merge_bar, drain[2];
-    int64_t first, last;                               // stream: the CTA's steps
-    StepAt at;
+    uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // [pipeline][step % 2]
+    uint64_t s_free[2], merge_bar, drain[2];
+    uint64_t ch_full[kChunks], ch_empty[kChunks];
+    Chunk ch[kChunks];
     uint32_t tmem_base;
     int abort_flag;
 };
@@ -76,75 +107,70 @@ struct FwdParams {
     FwdPlan plan;
     __nv_bfloat16 *out;     // [rows of all][D]
     float *lse;             // nullable
-    float *part_o, *part_lse, *whole_o, *whole_lse;
+    float *part_o, *part_lse, *whole_o, *whole_lse;     // whole: null for a single set
+    Cut *cuts;              // [ctas]: single set
+    int2 *spans;            // [units]: two sets: first and last CTA of a unit
     int64_t all_rows;       // batch * kv_heads * rows
     float scale_log2;
     uint32_t *status;       // nullable
 };
 
 struct Maps {
-    CUtensorMap q[2], k[2], v[2];
+    CUtensorMap q, k, v;
 };
 
-// What a CTA does next: key tiles [t0, t0 + nt) of a unit. slot -1: the whole unit.
-struct Chunk {
-    int set, t0, nt, len, slot;
-    int64_t z, hk, pair;
-};
-struct Walk {
-    int set, t, steps;
-    int64_t z, uu, left;    // stream: steps left; whole: the unit's index
-};
-template <int D> __device__ __forceinline__ Walk walk_begin(const FwdParams &p, const Shared<D> &sh) {
-    Walk w;
+// Warp-wide (the scan of the sets' lengths).
+__device__ __forceinline__ Walk walk_begin(const FwdParams &p, int lane) {
+    Walk w{};
     if (p.plan.stream) {
-        w.set = sh.at.set;
-        w.t = sh.at.t;
-        w.steps = sh.at.steps;
-        w.z = sh.at.z;
-        w.uu = sh.at.uu;
-        w.left = sh.last - sh.first;
+        if (lane == 0 && p.cuts) p.cuts[blockIdx.x].last = -1;   // until one is noted
+        w.total = total_steps(p.plan, lane);
+        w.at = cta_first(blockIdx.x, w.total, p.plan.ctas);
+        w.left = cta_first(blockIdx.x + 1, w.total, p.plan.ctas) - w.at;
+        if (w.left > 0) {
+            const StepAt at = step_at(p.plan, w.at, lane);
+            w.t = at.t;
+            w.steps = at.steps;
+            w.z = at.z;
+            w.uu = at.uu;
+        }
     } else {
         w.left = blockIdx.x;
     }
     return w;
 }
-__device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c, uint32_t *status) {
+// The next chunk; a unit that begins here is noted for the join (by lane 0).
+__device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c, bool lead) {
+    const FwdSet &s = p.plan.s;
     int steps;
     if (p.plan.stream) {
         if (w.left <= 0) return false;
-        const FwdSet *s = &p.plan.s[w.set];
         if (w.t == w.steps) {                          // the next unit
             w.t = 0;
-            if (++w.uu == s->upz) {
+            if (++w.uu == s.upz) {
                 w.uu = 0;
-                if (++w.z == s->sets) {
-                    w.z = 0;
-                    if (++w.set == p.plan.nsets) return false;
-                    s = &p.plan.s[w.set];
-                }
-                w.steps = set_steps(*s, w.z);
+                ++w.z;
+                w.steps = set_steps(s, w.z);
             }
         }
-        c.set = w.set;
         c.z = w.z;
-        c.hk = w.uu / s->pairs;
-        c.pair = w.uu - c.hk * s->pairs;
+        c.hk = w.uu / s.pairs;
+        c.pair = w.uu - c.hk * s.pairs;
         c.t0 = w.t;
         steps = (int)min((int64_t)(w.steps - w.t), w.left);
         c.slot = steps == w.steps ? -1 : (w.t > 0 ? 0 : 1);
+        if (lead && w.t == 0) {
+            const int last = c.slot < 0 ? (int)blockIdx.x : cta_of(w.at + w.steps - 1, w.total, p.plan.ctas);
+            if (p.spans) p.spans[w.z * s.upz + w.uu] = make_int2(blockIdx.x, last);
+            else if (c.slot == 1) p.cuts[blockIdx.x] = Cut{(int)c.z, (int)c.hk, (int)c.pair, last};
+        }
         w.t += steps;
+        w.at += steps;
         w.left -= steps;
     } else {
         int64_t u = w.left;
-        c.set = 0;
-        const int64_t n0 = p.plan.s[0].sets * p.plan.s[0].upz;
-        if (u >= n0) {
-            u -= n0;
-            c.set = 1;
-            if (p.plan.nsets == 1 || u >= p.plan.s[1].sets * p.plan.s[1].upz) return false;
-        }
-        const FwdSet &s = p.plan.s[c.set];
+        if (u >= s.sets * s.upz) return false;
+        if (lead && p.spans) p.spans[u] = make_int2(0, 0);
         c.z = u / s.upz;
         u -= c.z * s.upz;
         c.hk = u / s.pairs;
@@ -154,45 +180,70 @@ __device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c,
         steps = 0x7fffffff;
         w.left += gridDim.x;
     }
-    const FwdSet &s = p.plan.s[c.set];
-    c.len = set_len(s.len, c.z, s.n, status);
-    const int tiles = (c.len + kTile - 1) / kTile;
+    const int len = set_len(s.len, c.z, s.n, lead ? p.status : nullptr), tiles = (len + kTile - 1) / kTile;
     c.nt = min(steps, tiles - c.t0);                   // 0 for a set without keys
+    c.rel = len - c.t0 * kTile;
+    c.alone = 2 * c.pair + 1 >= s.tiles;
     return true;
 }
 
-// Tiles in flight through the ring, in the order in which both pipelines take them: many rows and
-// D = 64: K0 K1 V0 K2 V1 ... (S of the next step goes before this one's P·V), else K0 V0 K1 V1 ...
-template <int D> __device__ __forceinline__ bool looks_ahead(bool few) { return D == 64 && !few; }
-
+// Warp 3: the CTA's chunks, a few ahead of the warps that work on them.
+template <int D> __device__ void chunk_role(const FwdParams &p, Shared<D> &sh, int lane) {
+    Walk w = walk_begin(p, lane);
+    for (uint32_t i = 0;; ++i) {
+        const int at = i % kChunks;
+        if (!__all_sync(0xffffffffu, wait_soon(&sh.ch_empty[at], ((i / kChunks) & 1) ^ 1, &sh.abort_flag, p.status))) return;
+        Chunk c{};
+        const bool more = walk_next(p, w, c, lane == 0);
+        if (!more) c.nt = -1;
+        if (lane == 0) {
+            sh.ch[at] = c;
+            mbar_arrive(&sh.ch_full[at]);
+        }
+        __syncwarp();
+        if (!more) return;
+    }
+}
+// The i-th chunk, or null at the end (and after a wait that expired: `ok` false).
 template <int D>
+__device__ __forceinline__ const Chunk *chunk_at(const FwdParams &p, Shared<D> &sh, uint32_t i, bool &ok) {
+    const int at = i % kChunks;
+    ok = __all_sync(0xffffffffu, wait_soon(&sh.ch_full[at], (i / kChunks) & 1, &sh.abort_flag, p.status));
+    return ok && sh.ch[at].nt >= 0 ? &sh.ch[at] : nullptr;
+}
+template <int D> __device__ __forceinline__ void chunk_done(Shared<D> &sh, uint32_t i, int lane) {
+    warp_arrive(&sh.ch_empty[i % kChunks], lane);
+}
+
+template <int D, bool FEW>
 __device__ void copy_role(const FwdParams &p, const Maps &maps, Shared<D> &sh, int lane) {
     using C = Cfg<D>;
     volatile int *abort_flag = &sh.abort_flag;
-    const bool leader = lane == 0;
+    const bool leader = elect_one();    // issues; the whole warp runs the loop
     auto wait_w = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     uint32_t pos = 0, nq[2] = {0, 0}, ntail = 0;
     bool ok = true;
-    Chunk c;
-    Walk w = walk_begin<D>(p, sh);
-    while (ok && walk_next(p, w, c, leader ? p.status : nullptr)) {
-        if (c.nt <= 0) continue;
-        const FwdSet &s = p.plan.s[c.set];
+    const Chunk *cp;
+    for (uint32_t i = 0; ok && (cp = chunk_at<D>(p, sh, i, ok)); ++i) {
+        const Chunk c = *cp;
+        chunk_done<D>(sh, i, lane);
+        if (c.nt == 0) continue;
+        const FwdSet &s = p.plan.s;
         for (int pl = 0; pl < 2 && ok; ++pl) {
-            const int64_t t = s.few ? 0 : 2 * c.pair + pl;
+            const int64_t t = FEW ? 0 : 2 * c.pair + pl;
             if (t >= s.tiles) continue;
             if (!(ok = wait_w(&sh.q_empty[pl], (nq[pl] & 1) ^ 1))) break;
             if (leader) {
                 const int64_t member = c.z * s.members + (s.bb ? t * s.bb : t / s.tpm);
                 const int row = s.bb ? 0 : (int)(t % s.tpm) * kTile;
                 const int box = (s.bb ? s.bb * (int)p.plan.rows : kTile) * 128;   // bytes of a copied box
-                const int reps = s.few ? 4 : 1;
+                const int reps = FEW ? 4 : 1;
                 mbar_expect_tx(&sh.q_full[pl], (uint32_t)(box * reps * C::HALVES));
                 for (int h = 0; h < C::HALVES; ++h)
                     for (int r = 0; r < reps; ++r)
-                        tma_load_4d(sh.q[pl] + h * (kTile * 128) + r * (32 * 128), &maps.q[c.set], &sh.q_full[pl],
+                        tma_load_4d(sh.q[pl] + h * (kTile * 128) + r * (32 * 128), &maps.q, &sh.q_full[pl],
                                     64 * h, row, (int)c.hk, (int)member);
             }
             __syncwarp();
@@ -205,7 +256,7 @@ __device__ void copy_role(const FwdParams &p, const Maps &maps, Shared<D> &sh, i
             if (!wait_w(&sh.kv_empty[st], ((pos / C::STAGES) & 1) ^ 1)) return false;
             const int row = (c.t0 + t) * kTile;
             // rows behind the length that are in the buffer (behind the buffer the copy fills zeros)
-            const int z0 = c.len - row, z1 = (int)min((int64_t)kTile, s.n - row);
+            const int z0 = c.rel - t * kTile, z1 = (int)min((int64_t)kTile, s.n - row);
             const bool zero = is_v && z0 < z1;
             uint64_t *bar = zero ? &sh.tail : &sh.kv_full[st];
             if (leader) {
@@ -234,16 +285,7 @@ __device__ void copy_role(const FwdParams &p, const Maps &maps, Shared<D> &sh, i
             return true;
         };
         if (!ok) break;
-        if (looks_ahead<D>(s.few)) {
-            if (!(ok = put(&maps.k[c.set], 0, false))) break;
-            for (int t = 0; t < c.nt && ok; ++t) {
-                if (t + 1 < c.nt && !(ok = put(&maps.k[c.set], t + 1, false))) break;
-                ok = put(&maps.v[c.set], t, true);
-            }
-        } else {
-            for (int t = 0; t < c.nt && ok; ++t)
-                ok = put(&maps.k[c.set], t, false) && put(&maps.v[c.set], t, true);
-        }
+        for (int t = 0; t < c.nt && ok; ++t) ok = put(&maps.k, t, false) && put(&maps.v, t, true);
     }
     if (!ok) {                              // let the copies in flight land before the CTA exits
         for (uint32_t i = pos > (uint32_t)C::STAGES ? pos - C::STAGES : 0; i < pos; ++i)
@@ -253,98 +295,119 @@ __device__ void copy_role(const FwdParams &p, const Maps &maps, Shared<D> &sh, i
     }
 }
 
-template <int D> __device__ __forceinline__ uint32_t col_s(int pl) { return 128u * pl; }
+__device__ __forceinline__ uint32_t col_s(int pl) { return 128u * pl; }
+template <int D, bool FEW> __device__ __forceinline__ uint32_t col_o(int pl) {
+    return FEW && D == 64 ? 384u + 64u * pl : 256u + (uint32_t)D * pl;
+}
+// few rows
 template <int D> __device__ __forceinline__ uint32_t col_p(int pl) { return D == 64 ? 256u + 64u * pl : 128u * pl; }
-template <int D> __device__ __forceinline__ uint32_t col_o(int pl) { return D == 64 ? 384u + 64u * pl : 256u + 128u * pl; }
 
-template <int D>
+// Steps of 64 keys of a chunk (many rows).
+__device__ __forceinline__ int sub_steps(int nt, int rel) { return (min(rel, nt * kTile) + kSub - 1) / kSub; }
+
+template <int D, bool FEW>
 __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int pl, int lane) {
     using C = Cfg<D>;
+    constexpr int KEYS = FEW ? kTile : kSub;           // keys of a step
     volatile int *abort_flag = &sh.abort_flag;
-    const bool leader = lane == 0;
-    const uint32_t tS = tmem + col_s<D>(pl), tP = tmem + col_p<D>(pl), tO = tmem + col_o<D>(pl);
+    const bool leader = elect_one();    // issues; the whole warp runs the loop
+    const uint32_t tS = tmem + col_s(pl), tP = FEW ? tmem + col_p<D>(pl) : tS, tO = tmem + col_o<D, FEW>(pl);
     const uint64_t dq = desc_kmajor_sw128(sh.q[pl]);
     const uint64_t dk0 = desc_kmajor_sw128(sh.kv[0]), dv0 = desc_mnmajor_sw128(sh.kv[0], kTile * 128);
     uint32_t pos = 0, g = 0, nq = 0;       // ring position, this pipeline's steps and units
     bool ok = true;
     auto wait_w = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(0xffffffffu, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
-    // a tile that only the other pipeline takes: released once it is there
-    auto skip = [&](uint32_t at) -> bool {
-        const int st = at % C::STAGES;
-        if (!wait_w(&sh.kv_full[st], (at / C::STAGES) & 1)) return false;
-        if (leader) mbar_arrive(&sh.kv_empty[st]);
-        __syncwarp();
-        return true;
+    auto there = [&](uint32_t at) -> bool { return wait_w(&sh.kv_full[at % C::STAGES], (at / C::STAGES) & 1); };
+    auto release = [&](int st, bool alone) {           // by the leader; alone: for the other pipeline too
+        commit(&sh.kv_empty[st]);
+        if (alone) commit(&sh.kv_empty[st]);
     };
-    auto issue_s = [&](uint32_t at, bool last) -> bool {
-        const int st = at % C::STAGES;
-        if (!wait_w(&sh.kv_full[st], (at / C::STAGES) & 1)) return false;
+    // S(gs) = Q·Kᵀ of KEYS keys from key `from` of the tile at ring position `at`, which is there
+    auto issue_s = [&](uint32_t gs, uint32_t at, int from, bool done, bool alone, bool last) {
+        const int st = at % C::STAGES, b = gs & 1;
         fence_after();
         if (leader) {
-            const uint64_t dk = dk0 + (uint64_t)st * (C::TILE >> 4);
+            const uint64_t dk = dk0 + (uint64_t)(st * (C::TILE >> 4) + from * 8);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t off = (kk / 4) * ((kTile * 128) >> 4) + 2 * (kk % 4);
-                mma_bf16(tS, dq + off, dk + off, idesc_of(128, false), kk > 0);
+                mma_bf16(tS + (FEW ? 0u : 64u * b), dq + off, dk + off, idesc_of(KEYS, false), kk > 0);
             }
-            commit(&sh.s_full[pl]);
-            commit(&sh.kv_empty[st]);
+            commit(&sh.s_full[pl][b]);
+            if (done) release(st, alone);
             if (last) commit(&sh.q_empty[pl]);
         }
         __syncwarp();
-        return true;
     };
-    auto issue_pv = [&](uint32_t at, bool first) -> bool {
-        const int st = at % C::STAGES;
-        if (!wait_w(&sh.p_full[pl], g & 1) || !wait_w(&sh.kv_full[st], (at / C::STAGES) & 1)) return false;
+    // O += P·V of step g once P is written; the tile at `at` is there
+    auto issue_pv = [&](uint32_t at, int from, bool done, bool alone, bool first) -> bool {
+        const int st = at % C::STAGES, b = g & 1;
+        if (!wait_w(&sh.p_full[pl][b], (g >> 1) & 1)) return false;
         fence_after();
         if (leader) {
-            const uint64_t dv = dv0 + (uint64_t)st * (C::TILE >> 4);
+            const uint64_t dv = dv0 + (uint64_t)(st * (C::TILE >> 4) + from * 8);
 #pragma unroll
-            for (int kk = 0; kk < kTile / 16; ++kk)
-                mma_ts(tO, tP + 8u * kk, dv + 128 * kk, idesc_of(D, true), (first && kk == 0) ? 0u : 1u);
-            commit(&sh.o_done[pl]);
-            commit(&sh.kv_empty[st]);
+            for (int kk = 0; kk < KEYS / 16; ++kk)
+                mma_ts(tO, tP + (FEW ? 0u : 64u * b) + 8u * kk, dv + 128 * kk, idesc_of(D, true), (first && kk == 0) ? 0u : 1u);
+            commit(&sh.o_done[pl][b]);
+            if (done) release(st, alone);
         }
         __syncwarp();
         ++g;
         return true;
     };
-    Chunk c;
-    Walk w = walk_begin<D>(p, sh);
-    while (ok && walk_next(p, w, c, nullptr)) {
-        if (c.nt <= 0) continue;
-        const FwdSet &s = p.plan.s[c.set];
-        const bool active = s.few || 2 * c.pair + pl < s.tiles;
-        if (active && !(ok = wait_w(&sh.q_full[pl], nq & 1))) break;
-        if (active) ++nq;
-        if (!active) {
-            for (int i = 0; i < 2 * c.nt && ok; ++i) ok = skip(pos + i);
-        } else if (s.few) {                 // alternate tiles; S of this pipeline's next tile after its P·V
-            // a pipeline without a tile of its own (one step) leaves Q unused
-            const int mine = (c.nt - pl + 1) / 2;
-            if (mine == 0 && leader) mbar_arrive(&sh.q_empty[pl]);
-            __syncwarp();
-            for (int t = 0; t < c.nt && ok; ++t) {
-                if ((t & 1) == pl)
-                    ok = issue_s(pos + 2 * t, t + 2 >= c.nt) && issue_pv(pos + 2 * t + 1, t == pl);
-                else
-                    ok = skip(pos + 2 * t) && skip(pos + 2 * t + 1);
+    const Chunk *cp;
+    for (uint32_t i = 0; ok && (cp = chunk_at<D>(p, sh, i, ok)); ++i) {
+        // uniform over the warp, for the compiler too: the MMAs' descriptors then need no vector registers
+        const int nt = uniform(cp->nt), rel = uniform(cp->rel);
+        const bool alone = FEW || uniform(cp->alone);  // no other pipeline takes these tiles
+        chunk_done<D>(sh, i, lane);
+        if (nt > 0 && (FEW || pl == 0 || !alone)) {
+            if (!(ok = wait_w(&sh.q_full[pl], nq & 1))) break;
+            ++nq;
+            if constexpr (FEW) {                       // every other tile
+                if (pl >= nt) {                        // one tile: this pipeline's Q stays unused
+                    if (leader) mbar_arrive(&sh.q_empty[pl]);
+                    __syncwarp();
+                } else {
+                    constexpr bool ahead = D == 64 && C::STAGES >= 6;
+                    if (!(ok = there(pos + 2 * pl))) break;
+                    issue_s(g, pos + 2 * pl, 0, true, true, pl + 2 >= nt);
+                    for (int t = pl; t < nt && ok; t += 2) {
+                        const bool more = t + 2 < nt;
+                        const uint32_t kn = pos + 2 * (t + 2), v = pos + 2 * t + 1;
+                        if (ahead) {                   // P has columns of its own: S as soon as the last one is read
+                            if (more) {
+                                if (!(ok = there(kn) && wait_w(&sh.s_free[pl], g & 1))) break;
+                                issue_s(g + 1, kn, 0, true, true, t + 4 >= nt);
+                            }
+                            ok = there(v) && issue_pv(v, 0, true, true, t == pl);
+                        } else {
+                            ok = there(v) && issue_pv(v, 0, true, true, t == pl) && (!more || there(kn));
+                            if (ok && more) issue_s(g, kn, 0, true, true, t + 4 >= nt);
+                        }
+                    }
+                }
+            } else {
+                const int n = sub_steps(nt, rel);
+                if (!(ok = there(pos))) break;
+                const uint32_t g0 = g;
+                auto s_step = [&](int u) {
+                    issue_s(g0 + u, pos + 2 * (u >> 1), kSub * (u & 1), (u & 1) || u + 1 == n, alone, u + 1 == n);
+                };
+                s_step(0);
+                if (n > 1) s_step(1);
+                for (int u = 0; u < n && ok; ++u) {
+                    const uint32_t v = pos + 2 * (u >> 1) + 1;
+                    ok = ((u & 1) || there(v)) && (u + 2 >= n || (u & 1) || there(pos + u + 2)) &&
+                         issue_pv(v, kSub * (u & 1), (u & 1) || u + 1 == n, alone, u == 0);
+                    if (ok && u + 2 < n) s_step(u + 2);
+                }
             }
-        } else if (looks_ahead<D>(false)) {
-            ok = issue_s(pos, c.nt == 1);
-            for (int t = 0; t < c.nt && ok; ++t) {
-                if (t + 1 < c.nt)
-                    ok = wait_w(&sh.s_free[pl], g & 1) && issue_s(pos + 2 * t + 1, t + 2 == c.nt);
-                ok = ok && issue_pv(pos + (t + 1 < c.nt ? 2 * t + 2 : 2 * t + 1), t == 0);
-            }
-        } else {
-            for (int t = 0; t < c.nt && ok; ++t)
-                ok = issue_s(pos + 2 * t, t + 1 == c.nt) && issue_pv(pos + 2 * t + 1, t == 0);
         }
-        pos += 2 * c.nt;
+        pos += 2 * nt;
     }
     // every MMA this warp issued must be complete before TMEM is freed
     if (leader) commit(&sh.drain[pl]);
@@ -359,18 +422,30 @@ __device__ __forceinline__ float max32(const float *s) {
     return fmax3(fmax3(a[0], a[1], a[2]), fmax3(a[3], a[4], a[5]), fmaxf(a[6], a[7]));
 }
 
-// 32 scores of a row to bf16 pairs of 2^(s·sl2 - m), and their sum onto acc.
-__device__ __forceinline__ void numerators32(const float *s, float sl2, float neg_m, uint32_t *pk, float2 &acc) {
+__device__ __forceinline__ float sum4(const float2 *a) {
+    const float2 t = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
+    return t.x + t.y;
+}
+// 32 scores of a row to bf16 pairs of 2^(s·sl2 - m), and their sums onto acc. GRP pairs at a time, in
+// three phases (exponents, exponentials, then packing and four chains of sums), so that in-order issue
+// does not wait on one result while independent work could be queued. POLY of 16 pairs take the
+// polynomial on the FMA pipe instead of the exp unit.
+template <int POLY>
+__device__ __forceinline__ void numerators32(const float *s, float sl2, float neg_m, uint32_t *pk, float2 *acc) {
     const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(neg_m, neg_m);
-    float2 x[16];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) x[c] = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sc2, nm2);
+    for (int h = 0; h < 16; h += GRP) {
+        float2 x[GRP];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) x[c] = make_float2(ex2(x[c].x), ex2(x[c].y));
+        for (int c = 0; c < GRP; ++c) x[c] = __ffma2_rn(make_float2(s[2 * (h + c)], s[2 * (h + c) + 1]), sc2, nm2);
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-        pk[c] = pack_bf16x2(x[c].x, x[c].y);
-        acc = __fadd2_rn(acc, x[c]);
+        for (int c = 0; c < GRP; ++c)
+            x[c] = (h + c) * POLY % 16 < POLY ? exp2_fma2(x[c]) : make_float2(ex2(x[c].x), ex2(x[c].y));
+#pragma unroll
+        for (int c = 0; c < GRP; ++c) {
+            pk[h + c] = pack_bf16x2(x[c].x, x[c].y);
+            acc[c & 3] = __fadd2_rn(acc[c & 3], x[c]);
+        }
     }
 }
 
@@ -400,7 +475,7 @@ struct RowOut {
 template <int D>
 __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, int64_t tile, int i_tile, int i_unit) {
     RowOut r;
-    const int64_t row = plan_row(p.plan, p.plan.s[c.set], c.z, c.hk, tile, i_tile);
+    const int64_t row = plan_row(p.plan, c.z, c.hk, tile, i_tile);
     r.valid = row >= 0;
     r.o16 = nullptr;
     r.o32 = r.lse = nullptr;
@@ -411,7 +486,7 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
         r.o32 = p.part_o + at * D;
         r.lse = p.part_lse + at;
     } else if (p.whole_o) {
-        const int64_t at = c.set * p.all_rows + row;
+        const int64_t at = row;
         r.o32 = p.whole_o + at * D;
         r.lse = p.whole_lse + at;
     } else {
@@ -422,130 +497,128 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
     return r;
 }
 
-template <int D>
+template <int D, bool FEW>
 __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int pl, int wq, int lane) {
     using C = Cfg<D>;
     const unsigned FULL = 0xffffffffu;
     volatile int *abort_flag = &sh.abort_flag;
     const uint32_t wl = (uint32_t)(32 * wq) << 16;
-    const uint32_t tS = tmem + col_s<D>(pl) + wl, tP = tmem + col_p<D>(pl) + wl, tO = tmem + col_o<D>(pl) + wl;
+    const uint32_t tS = tmem + col_s(pl) + wl, tO = tmem + col_o<D, FEW>(pl) + wl;
     const float sl2 = p.scale_log2;
     uint32_t g = 0, nmerge = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t *b, uint32_t par) -> bool {
-        return __all_sync(FULL, wait_fast(b, par, abort_flag, p.status));
+        return __all_sync(FULL, wait_soon(b, par, abort_flag, p.status));
     };
-    // running maximum m (lazy) and sum l of this thread's row; O is rescaled when m grows by 2^8
-    auto new_max = [&](float mx, float &m, float &l, bool started) {
+    // the P·V of the step before this one is complete
+    auto wait_o = [&]() -> bool { return wait_all(&sh.o_done[pl][(g - 1) & 1], ((g - 1) >> 1) & 1); };
+    // running maximum m (lazy) and sum l of this thread's row; when m grows by 2^8, O is rescaled, once
+    // the P·V of the step before (`started`) is complete
+    auto new_max = [&](float mx, float &m, float &l, bool started) -> bool {
         const bool first = m == -CUDART_INF_F;
         const bool need = !first && mx > m + kRescaleLog2;
         if (__any_sync(FULL, need) && started) {
+            if (!wait_o()) return false;
             const float alpha = need ? ex2(m - mx) : 1.f;
             fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
+            for (int cc = 0; cc < D; cc += 32) {
                 float o[32];
-                tmem_ld32(tO + 32 * cc, o);
+                tmem_ld32(tO + cc, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                tmem_st32(tO + 32 * cc, o);
+                tmem_st32(tO + cc, o);
             }
             tmem_wait_st();
             l *= alpha;
         }
         if (first || need) m = mx;
+        return true;
     };
-    Chunk c;
-    Walk w = walk_begin<D>(p, sh);
-    while (ok && walk_next(p, w, c, nullptr)) {
-        const FwdSet &s = p.plan.s[c.set];
+    const Chunk *cp;
+    for (uint32_t i = 0; ok && (cp = chunk_at<D>(p, sh, i, ok)); ++i) {
+        const int nt = uniform(cp->nt), rel = uniform(cp->rel);
         float m = -CUDART_INF_F, l = 0.f;
-        if (!s.few) {
-            const int64_t tile = 2 * c.pair + pl;
-            if (tile >= s.tiles) continue;
-            for (int t = 0; t < c.nt; ++t, ++g) {
-                if (!(ok = wait_all(&sh.s_full[pl], g & 1))) break;
+        if constexpr (!FEW) {
+            if (pl == 1 && cp->alone) {
+                chunk_done<D>(sh, i, lane);
+                continue;
+            }
+            const int n = nt > 0 ? sub_steps(nt, rel) : 0;
+            for (int u = 0; u < n; ++u, ++g) {
+                const uint32_t tSu = tS + 64u * (g & 1);
+                if (!(ok = wait_all(&sh.s_full[pl][g & 1], (g >> 1) & 1))) break;
                 fence_after();
-                float x[128];
+                float x[kSub];
+                tmem_ld32(tSu, x);
+                tmem_ld32(tSu + 32, x + 32);
+                tmem_wait_ld_of(x);
+                const int valid = rel - u * kSub;      // keys behind the length count as -inf
+                if (valid < kSub) {
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) tmem_ld32(tS + 32 * cc, x + 32 * cc);
-                tmem_wait_ld();
-                if constexpr (D == 64) {
-                    fence_before();
-                    mbar_arrive(&sh.s_free[pl]);
+                    for (int e = 0; e < kSub; ++e) x[e] = e < valid ? x[e] : -CUDART_INF_F;
                 }
-                const int valid = c.len - (c.t0 + t) * kTile;
-                if (valid < kTile) {
-#pragma unroll
-                    for (int e = 0; e < 128; ++e) x[e] = e < valid ? x[e] : -CUDART_INF_F;
-                }
-                const float mx = sl2 * fmaxf(fmaxf(max32(x), max32(x + 32)), fmaxf(max32(x + 64), max32(x + 96)));
-                // P·V of the step before has read P and written O
-                if (t > 0 && !(ok = wait_all(&sh.o_done[pl], (g - 1) & 1))) break;
-                new_max(mx, m, l, t > 0);
+                if (!(ok = new_max(sl2 * fmaxf(max32(x), max32(x + 32)), m, l, u > 0))) break;
                 const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
-                float2 acc = make_float2(0.f, 0.f);
+                float2 acc[4] = {};
 #pragma unroll
-                for (int cc = 0; cc < 4; ++cc) {
+                for (int h = 0; h < 2; ++h) {
                     uint32_t pk[16];
-                    numerators32(x + 32 * cc, sl2, neg_m, pk, acc);
-                    tmem_st16w(tP + 16 * cc, pk);
+                    numerators32<kPoly<D>>(x + 32 * h, sl2, neg_m, pk, acc);
+                    tmem_st16w(tSu + 16 * h, pk);
                 }
-                l += acc.x + acc.y;
+                l += sum4(acc);
                 tmem_wait_st();
                 fence_before();
-                mbar_arrive(&sh.p_full[pl]);
+                warp_arrive(&sh.p_full[pl][g & 1], lane);
             }
-            if (!ok || (c.nt > 0 && !(ok = wait_all(&sh.o_done[pl], (g - 1) & 1)))) break;
+            if (!ok || (n > 0 && !(ok = wait_o()))) break;
             fence_after();
-            const RowOut r = row_out<D>(p, c, tile, 32 * wq + lane, kTile * pl + 32 * wq + lane);
+            const RowOut r = row_out<D>(p, *cp, 2 * cp->pair + pl, 32 * wq + lane, kTile * pl + 32 * wq + lane);
             const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
+            for (int cc = 0; cc < D; cc += 32) {
                 float o[32];
-                if (c.nt > 0) {
-                    tmem_ld32(tO + 32 * cc, o);
+                if (n > 0) {
+                    tmem_ld32(tO + cc, o);
                     tmem_wait_ld();
-                } else {
+                }
+                if (n == 0 || l == 0.f) {
 #pragma unroll
                     for (int e = 0; e < 32; ++e) o[e] = 0.f;
                 }
-                if (l == 0.f) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                }
-                if (r.valid) store32(r.o16 ? r.o16 + 32 * cc : nullptr, r.o32 + 32 * cc, o, inv);
+                if (r.valid) store32(r.o16 ? r.o16 + cc : nullptr, r.o32 + cc, o, inv);
             }
             if (r.valid && r.lse) *r.lse = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * r.lse_unit;
             fence_before();
-            continue;
-        }
+            chunk_done<D>(sh, i, lane);
+        } else {
+        const uint32_t tP = tmem + col_p<D>(pl) + wl;
         // few rows: this warp's keys are 32·wq .. +31 of each of its pipeline's tiles
-        const int nrows = (int)(s.members * p.plan.rows);
+        const int nrows = (int)(p.plan.s.members * p.plan.rows);
         bool any = false;
-        for (int t = pl; t < c.nt; t += 2, ++g) {
-            if (!(ok = wait_all(&sh.s_full[pl], g & 1))) break;
+        for (int t = pl; t < nt; t += 2, ++g) {
+            if (!(ok = wait_all(&sh.s_full[pl][g & 1], (g >> 1) & 1))) break;
             fence_after();
             float x[32];
             tmem_ld32(tS + 32 * wq, x);
             tmem_wait_ld();
-            if constexpr (D == 64) {
-                fence_before();
-                mbar_arrive(&sh.s_free[pl]);
-            }
-            const int valid = c.len - (c.t0 + t) * kTile - 32 * wq;
+            fence_before();
+            warp_arrive(&sh.s_free[pl], lane);
+            const int valid = rel - t * kTile - 32 * wq;
             if (valid < 32) {
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[e] = e < valid ? x[e] : -CUDART_INF_F;
             }
             const float mx = sl2 * max32(x);
-            if (any && !(ok = wait_all(&sh.o_done[pl], (g - 1) & 1))) break;
-            new_max(mx, m, l, any);
-            any = true;
-            float2 acc = make_float2(0.f, 0.f);
+            if (!(ok = new_max(mx, m, l, any))) break;
+            float2 acc[4] = {};
             uint32_t pk[16], zero[16];
-            numerators32(x, sl2, m == -CUDART_INF_F ? 0.f : -m, pk, acc);
+            numerators32<0>(x, sl2, m == -CUDART_INF_F ? 0.f : -m, pk, acc);
+            if (D == 64 && any && !(ok = wait_o())) break;   // P is read
+            any = true;
+            fence_after();
 #pragma unroll
             for (int e = 0; e < 16; ++e) zero[e] = 0u;
 #pragma unroll
@@ -553,27 +626,27 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 if (cc == wq) tmem_st16w(tP + 16 * cc, pk);
                 else tmem_st16w(tP + 16 * cc, zero);
             }
-            l += acc.x + acc.y;
+            l += sum4(acc);
             tmem_wait_st();
             fence_before();
-            mbar_arrive(&sh.p_full[pl]);
+            warp_arrive(&sh.p_full[pl][g & 1], lane);
         }
-        if (!ok || (any && !(ok = wait_all(&sh.o_done[pl], (g - 1) & 1)))) break;
+        if (!ok || (any && !(ok = wait_o()))) break;
         fence_after();
         // merge the eight partial rows: weights 2^(m - M) / L, then sums through shared memory. A row
         // that is not one of the unit's (lane >= nrows) holds whatever it holds and is not stored.
         const int idx = 4 * pl + wq;
         sh.ml[0][idx][lane] = m;
         sh.ml[1][idx][lane] = l;
-        mbar_arrive(&sh.merge_bar);
+        warp_arrive(&sh.merge_bar, lane);
         if (!(ok = wait_all(&sh.merge_bar, nmerge++ & 1))) break;
         float M = -CUDART_INF_F, L = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) M = fmaxf(M, sh.ml[0][i][lane]);
+        for (int k = 0; k < 8; ++k) M = fmaxf(M, sh.ml[0][k][lane]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float li = sh.ml[1][i][lane];
-            L += li == 0.f ? 0.f : li * ex2(sh.ml[0][i][lane] - M);
+        for (int k = 0; k < 8; ++k) {
+            const float lk = sh.ml[1][k][lane];
+            L += lk == 0.f ? 0.f : lk * ex2(sh.ml[0][k][lane] - M);
         }
         const float f = l == 0.f ? 0.f : ex2(m - M) / L;
         for (int r0 = 0; r0 < nrows; r0 += C::MROWS) {
@@ -594,21 +667,21 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 }
                 __syncwarp();
             }
-            mbar_arrive(&sh.merge_bar);
+            warp_arrive(&sh.merge_bar, lane);
             if (!(ok = wait_all(&sh.merge_bar, nmerge++ & 1))) break;
             {   // MROWS·D/4 groups of four columns (128 or 256): one a thread
-                const int at = 128 * pl + 32 * wq + lane, i = at / (D / 4), col = 4 * (at % (D / 4));
-                if (i < C::MROWS && r0 + i < nrows) {
+                const int at = 128 * pl + 32 * wq + lane, mr = at / (D / 4), col = 4 * (at % (D / 4));
+                if (mr < C::MROWS && r0 + mr < nrows) {
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const float4 z = *reinterpret_cast<const float4 *>(&sh.merge[k][i][col]);
+                        const float4 z = *reinterpret_cast<const float4 *>(&sh.merge[k][mr][col]);
                         y.x += z.x;
                         y.y += z.y;
                         y.z += z.z;
                         y.w += z.w;
                     }
-                    const RowOut r = row_out<D>(p, c, 0, r0 + i, r0 + i);
+                    const RowOut r = row_out<D>(p, *cp, 0, r0 + mr, r0 + mr);
                     if (r.valid) {
                         if (r.o16)
                             *reinterpret_cast<uint2 *>(r.o16 + col) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
@@ -617,41 +690,49 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                     }
                 }
             }
-            mbar_arrive(&sh.merge_bar);    // the buffer is free again
+            warp_arrive(&sh.merge_bar, lane);    // the buffer is free again
             if (!(ok = wait_all(&sh.merge_bar, nmerge++ & 1))) break;
         }
         if (!ok) break;
         if (idx == 0 && lane < nrows) {
-            const RowOut r = row_out<D>(p, c, 0, lane, lane);
+            const RowOut r = row_out<D>(p, *cp, 0, lane, lane);
             if (r.valid && r.lse) *r.lse = L == 0.f ? -CUDART_INF_F : (M + __log2f(L)) * r.lse_unit;
         }
         fence_before();
+        chunk_done<D>(sh, i, lane);
+        }
     }
 }
 
-template <int D>
+template <int D, bool FEW>
 __global__ void __launch_bounds__(NTHREADS, 1) dense_fwd_kernel(const __grid_constant__ Maps maps,
                                                                 const __grid_constant__ FwdParams p) {
     extern __shared__ uint8_t smem_raw[];
     Shared<D> &sh = *reinterpret_cast<Shared<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         sh.abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_empty[i], 1);
-            mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_free[i], 128);
-            mbar_init(&sh.p_full[i], 128);
-            mbar_init(&sh.o_done[i], 1);
+            mbar_init(&sh.s_free[i], 4);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(&sh.s_full[i][b], 1);
+                mbar_init(&sh.p_full[i][b], 4);
+                mbar_init(&sh.o_done[i][b], 1);
+            }
             mbar_init(&sh.drain[i], 1);
         }
         for (int i = 0; i < Cfg<D>::STAGES; ++i) {
             mbar_init(&sh.kv_full[i], 1);
             mbar_init(&sh.kv_empty[i], 2);
         }
+        for (int i = 0; i < kChunks; ++i) {
+            mbar_init(&sh.ch_full[i], 1);
+            mbar_init(&sh.ch_empty[i], kReaders);
+        }
         mbar_init(&sh.tail, 1);
-        mbar_init(&sh.merge_bar, 256);
+        mbar_init(&sh.merge_bar, 8);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
@@ -659,28 +740,18 @@ __global__ void __launch_bounds__(NTHREADS, 1) dense_fwd_kernel(const __grid_con
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    if (warp == 3 && p.plan.stream) {
-        const int64_t total = total_steps(p.plan, lane);
-        const int64_t first = cta_first(blockIdx.x, total, p.plan.ctas), last = cta_first(blockIdx.x + 1, total, p.plan.ctas);
-        StepAt at{};
-        if (first < last) at = step_at(p.plan, first, lane);
-        if (lane == 0) {
-            sh.first = first;
-            sh.last = last;
-            sh.at = at;
-        }
-    }
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = sh.tmem_base;
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
-        if (warp == 0) copy_role<D>(p, maps, sh, lane);
-        else if (warp < 3) mma_role<D>(p, sh, tmem, warp - 1, lane);
+        if (warp == 0) copy_role<D, FEW>(p, maps, sh, lane);
+        else if (warp < 3) mma_role<D, FEW>(p, sh, tmem, warp - 1, lane);
+        else chunk_role<D>(p, sh, lane);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        softmax_role<D>(p, sh, tmem, (warp - 4) >> 2, warp & 3, lane);
+        softmax_role<D, FEW>(p, sh, tmem, (warp - 4) >> 2, warp & 3, lane);
     }
     __syncwarp();
     fence_before();
@@ -693,135 +764,177 @@ __global__ void __launch_bounds__(NTHREADS, 1) dense_fwd_kernel(const __grid_con
 
 // ---------------------------------------------------------------- join
 
-// The parts of one unit's row, weighted by 2^(lse - max): o = Σ w_p o_p / Σ w_p. One warp a row;
-// lane holds columns lane·D/32.. of the sum. Parts come in the order of their CTAs.
+// Rows of several parts, one after the other: o = Σ w_p o_p / Σ w_p with w_p = 2^(lse_p - max). A warp
+// has a row, lane l its columns l·D/32..; a part's lse is read by one lane, 32 parts at a time, so
+// that all weights are known before the parts' rows, whose loads then do not wait for one another.
 template <int D> struct Joined {
     float o[D / 32], m, l;
 };
-template <int D> __device__ __forceinline__ void join_add(Joined<D> &j, const float *o, float lse, int lane) {
-    if (lse == -CUDART_INF_F) return;
-    const float mn = fmaxf(j.m, lse);
-    const float a = j.m == -CUDART_INF_F ? 0.f : exp2f(j.m - mn), b = exp2f(lse - mn);
-    float x[D / 32];
-    if constexpr (D == 64) {
-        const float2 y = *reinterpret_cast<const float2 *>(o + 2 * lane);
-        x[0] = y.x, x[1] = y.y;
-    } else {
-        const float4 y = *reinterpret_cast<const float4 *>(o + 4 * lane);
-        x[0] = y.x, x[1] = y.y, x[2] = y.z, x[3] = y.w;
-    }
-#pragma unroll
-    for (int e = 0; e < D / 32; ++e) j.o[e] = j.o[e] * a + x[e] * b;
-    j.l = j.l * a + b;
-    j.m = mn;
-}
-template <int D> __device__ __forceinline__ void join_store(const FwdParams &p, const Joined<D> &j, int64_t row, int lane) {
-    const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
-    uint32_t u[D / 64];
-#pragma unroll
-    for (int e = 0; e < D / 64; ++e) u[e] = pack_bf16x2(j.o[2 * e] * inv, j.o[2 * e + 1] * inv);
-    if constexpr (D == 64) reinterpret_cast<uint32_t *>(p.out + row * D)[lane] = u[0];
-    else reinterpret_cast<uint2 *>(p.out + row * D)[lane] = make_uint2(u[0], u[1]);
-    if (p.lse && lane == 0) p.lse[row] = j.l == 0.f ? -CUDART_INF_F : (j.m + __log2f(j.l)) * kLn2;
-}
 template <int D> __device__ __forceinline__ void join_begin(Joined<D> &j) {
     j.m = -CUDART_INF_F;
     j.l = 0.f;
 #pragma unroll
     for (int e = 0; e < D / 32; ++e) j.o[e] = 0.f;
 }
-// All parts of row i (of the unit's 256), begun by CTA ca and ended by CTA cb. With fewer steps than
-// CTAs some of those in between have none.
+// `count` parts; part k's row is number row_of(k) of o and lse.
+template <int D, typename F>
+__device__ __forceinline__ void join_add(Joined<D> &j, const float *o, const float *lse, int count, F row_of, int lane) {
+    for (int k0 = 0; k0 < count; k0 += 32) {
+        const int k = k0 + lane, n = min(32, count - k0);
+        const float mine = k < count ? __ldg(lse + row_of(k)) : -CUDART_INF_F;
+        float mx = mine;
+        for (int i = 16; i; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
+        const float mn = fmaxf(j.m, mx);
+        if (mn == -CUDART_INF_F) continue;             // no keys in any part so far
+        const float a = ex2(j.m - mn), wt = ex2(mine - mn);
+        float sum = wt;
+        for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);
+        j.l = j.l * a + sum;
+        j.m = mn;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) j.o[e] *= a;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float w = __shfl_sync(0xffffffffu, wt, i);
+            const float *src = o + row_of(k0 + i) * D;
+            if (w == 0.f) continue;                    // its row may never have been written
+            if constexpr (D == 64) {
+                const float2 y = *reinterpret_cast<const float2 *>(src + 2 * lane);
+                j.o[0] = fmaf(y.x, w, j.o[0]), j.o[1] = fmaf(y.y, w, j.o[1]);
+            } else {
+                const float4 y = *reinterpret_cast<const float4 *>(src + 4 * lane);
+                j.o[0] = fmaf(y.x, w, j.o[0]), j.o[1] = fmaf(y.y, w, j.o[1]);
+                j.o[2] = fmaf(y.z, w, j.o[2]), j.o[3] = fmaf(y.w, w, j.o[3]);
+            }
+        }
+    }
+}
 template <int D>
-__device__ __forceinline__ void join_parts(const FwdParams &p, Joined<D> &j, int ca, int cb, int i, int64_t total,
-                                           int lane) {
-    for (int c = ca; c <= cb; ++c) {
-        if (total < p.plan.ctas && cta_first(c, total, p.plan.ctas) == cta_first(c + 1, total, p.plan.ctas)) continue;
-        const int64_t at = (2 * (int64_t)c + (c == ca)) * (2 * kTile) + i;
-        join_add<D>(j, p.part_o + at * D, p.part_lse[at], lane);
+__device__ __forceinline__ void join_store(const Joined<D> &j, __nv_bfloat16 *out, float *lse, int64_t row, int lane) {
+    const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
+    uint32_t u[D / 64];
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) u[e] = pack_bf16x2(j.o[2 * e] * inv, j.o[2 * e + 1] * inv);
+    if constexpr (D == 64) reinterpret_cast<uint32_t *>(out + row * D)[lane] = u[0];
+    else reinterpret_cast<uint2 *>(out + row * D)[lane] = make_uint2(u[0], u[1]);
+    if (lse && lane == 0) lse[row] = j.l == 0.f ? -CUDART_INF_F : (j.m + __log2f(j.l)) * kLn2;
+}
+// Row i (of a unit's 256) of the parts that CTA ca begins: number of the k-th part's row.
+struct PartRow {
+    int ca, i;
+    __device__ int64_t operator()(int k) const { return (2 * ((int64_t)ca + k) + (k == 0)) * (2 * kTile) + i; }
+};
+
+// A single set: block (c, y) joins rows of the unit that CTA c begins and leaves, if there is one; the
+// other units' rows were finished by the one CTA that had them. Units of many rows are cut into two
+// or three parts as a rule: then a warp has four rows, and all their parts' loads go out together.
+constexpr int kJoinRows = 4, kJoinParts = 4;
+template <int D> __global__ void __launch_bounds__(256) join_cut_kernel(const __grid_constant__ FwdParams p, int each) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, ca = blockIdx.x;
+    const Cut cut = p.cuts[ca];
+    if (cut.last < ca || cut.last >= p.plan.ctas) return;
+    const int count = cut.last - ca + 1, i0 = (8 * blockIdx.y + warp) * each;
+    auto row_at = [&](int i) -> int64_t {
+        const int64_t t = 2 * (int64_t)cut.tile + i / kTile;
+        return t < p.plan.s.tiles ? plan_row(p.plan, cut.z, cut.hk, t, i % kTile) : -1;
+    };
+    const int64_t mine = lane < each ? row_at(i0 + lane) : -1;     // the warp's rows, one a lane
+    if (each == kJoinRows && count <= kJoinParts) {
+        using V = typename std::conditional<D == 64, float2, float4>::type;
+        V y[kJoinRows][kJoinParts];
+        float ls[kJoinRows][kJoinParts];
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+            const bool there = __shfl_sync(0xffffffffu, mine, r) >= 0;
+#pragma unroll
+            for (int k = 0; k < kJoinParts; ++k) {
+                ls[r][k] = -CUDART_INF_F;
+                if (there && k < count) {
+                    const int64_t at = PartRow{ca, i0 + r}(k);
+                    ls[r][k] = __ldg(p.part_lse + at);
+                    y[r][k] = __ldg(reinterpret_cast<const V *>(p.part_o + at * D) + lane);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < kJoinRows; ++r) {
+            const int64_t row = __shfl_sync(0xffffffffu, mine, r);
+            if (row < 0) continue;
+            Joined<D> j;
+            join_begin<D>(j);
+            j.m = fmaxf(fmaxf(ls[r][0], ls[r][1]), fmaxf(ls[r][2], ls[r][3]));
+#pragma unroll
+            for (int k = 0; k < kJoinParts; ++k) {
+                if (ls[r][k] == -CUDART_INF_F) continue;
+                const float w = ex2(ls[r][k] - j.m);
+                j.l += w;
+                j.o[0] = fmaf(y[r][k].x, w, j.o[0]), j.o[1] = fmaf(y[r][k].y, w, j.o[1]);
+                if constexpr (D == 128) j.o[2] = fmaf(y[r][k].z, w, j.o[2]), j.o[3] = fmaf(y[r][k].w, w, j.o[3]);
+            }
+            join_store<D>(j, p.out, p.lse, row, lane);
+        }
+        return;
+    }
+    for (int i = i0; i < i0 + each; ++i) {
+        const int64_t row = __shfl_sync(0xffffffffu, mine, i - i0);
+        if (row < 0) continue;
+        Joined<D> j;
+        join_begin<D>(j);
+        join_add<D>(j, p.part_o, p.part_lse, count, PartRow{ca, i}, lane);
+        join_store<D>(j, p.out, p.lse, row, lane);
     }
 }
 
-// One set: a block joins 8 rows of the unit in which CTA blockIdx.x + 1 begins, if it is the first
-// CTA to begin inside that unit. The other units' rows were finished by the one CTA that had them.
-template <int D> __global__ void __launch_bounds__(256) join_one_kernel(const __grid_constant__ FwdParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = blockIdx.x + 1;
-    const int64_t total = total_steps(p.plan, lane), x = cta_first(c, total, p.plan.ctas);
-    if (x >= total) return;
-    const StepAt at = step_at(p.plan, x, lane);
-    if (at.t == 0) return;
-    const int64_t a = x - at.t;
-    if (cta_of(a, total, p.plan.ctas) != c - 1) return;
-    const FwdSet &s = p.plan.s[0];
-    const int i = 8 * blockIdx.y + warp;
-    const int64_t hk = at.uu / s.pairs, pair = at.uu - hk * s.pairs;
-    const int64_t row = s.few ? plan_row(p.plan, s, at.z, hk, 0, i)
-                              : (2 * pair + i / kTile < s.tiles ? plan_row(p.plan, s, at.z, hk, 2 * pair + i / kTile, i % kTile) : -1);
-    if (row < 0) return;
-    Joined<D> j;
-    join_begin<D>(j);
-    join_parts<D>(p, j, c - 1, cta_of(a + at.steps - 1, total, p.plan.ctas), i, total, lane);
-    join_store<D>(p, j, row, lane);
-}
-
 // Two sets: a warp joins one row's parts of both.
-template <int D> __global__ void __launch_bounds__(256) join_two_kernel(const __grid_constant__ FwdParams p) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+template <int D>
+__global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ FwdParams p0, const __grid_constant__ FwdParams p1) {
+    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
     const int64_t row = (int64_t)blockIdx.x * 8 + warp;
-    if (row >= p.all_rows) return;
-    const int64_t slab = row / p.plan.rows, r = row - slab * p.plan.rows, b = slab / p.plan.kv_heads;
-    const int64_t hk = slab - b * p.plan.kv_heads;
-    const int64_t total = p.plan.stream ? total_steps(p.plan, lane) : 0;
-    int64_t base = 0;
+    if (row >= p0.all_rows) return;
+    // 32-bit divisions where they do: rows of a slab, members and tiles of a set are far below 2^31
+    const uint32_t slab = (uint32_t)(row / p0.plan.rows), b = slab / (uint32_t)p0.plan.kv_heads;
+    const uint32_t r = (uint32_t)(row - (int64_t)slab * p0.plan.rows), hk = slab - b * (uint32_t)p0.plan.kv_heads;
     Joined<D> j;
     join_begin<D>(j);
+#pragma unroll
     for (int k = 0; k < 2; ++k) {
-        const FwdSet &s = p.plan.s[k];
-        const int64_t z = b / s.members, member = b - z * s.members;
-        int64_t t, i;
+        const FwdParams &p = k ? p1 : p0;
+        const FwdSet &s = p.plan.s;
+        const uint32_t z = b / (uint32_t)s.members, member = b - z * (uint32_t)s.members;
+        uint32_t t, i;
         if (s.bb) {
-            t = member / s.bb;
-            i = (member - t * s.bb) * p.plan.rows + r;
+            t = member / (uint32_t)s.bb;
+            i = (member - t * s.bb) * (uint32_t)p.plan.rows + r;
         } else {
             t = member * s.tpm + r / kTile;
             i = r % kTile;
         }
-        bool whole = true;
-        if (p.plan.stream) {
-            const int steps = set_steps(s, z);
-            const int64_t a = base + steps_before(s, z, lane) + (hk * s.pairs + t / 2) * steps;
-            const int ca = cta_of(a, total, p.plan.ctas), cb = cta_of(a + steps - 1, total, p.plan.ctas);
-            whole = ca == cb;
-            if (!whole) join_parts<D>(p, j, ca, cb, (int)(s.few ? i : i + kTile * (t & 1)), total, lane);
-            base += steps_before(s, s.sets, lane);
-        }
-        if (whole) {
-            const int64_t at = k * p.all_rows + row;
-            join_add<D>(j, p.whole_o + at * D, p.whole_lse[at], lane);
-        }
+        const int2 span = p.spans[z * s.upz + hk * s.pairs + t / 2];
+        // (after an expired wait a span may be missing; what it holds then must not lead out of the parts)
+        if (span.x < 0 || span.y < span.x || span.y >= p.plan.ctas) continue;
+        if (span.x == span.y)
+            join_add<D>(j, p.whole_o, p.whole_lse, 1, [row](int) { return row; }, lane);
+        else
+            join_add<D>(j, p.part_o, p.part_lse, span.y - span.x + 1, PartRow{span.x, (int)(i + kTile * (t & 1))}, lane);
     }
-    join_store<D>(p, j, row, lane);
+    join_store<D>(j, p0.out, nullptr, row, lane);
 }
 
 // ---------------------------------------------------------------- host
 
-template <int D>
-cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet *sets, FwdParams &p, cudaStream_t stream) {
+template <int D, bool FEW> cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, const FwdParams &p, cudaStream_t stream) {
     Maps maps;
-    for (int k = 0; k < 2; ++k) {
-        const KeySet &ks = sets[k < p.plan.nsets ? k : 0];
-        const FwdSet &s = p.plan.s[k < p.plan.nsets ? k : 0];
-        const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)pb.rows, (cuuint64_t)pb.kv_heads, (cuuint64_t)pb.batch};
-        const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)pb.rows * D * 2, (cuuint64_t)pb.kv_heads * pb.rows * D * 2};
-        const cuuint32_t qb[4] = {64, s.bb ? (cuuint32_t)pb.rows : (cuuint32_t)kTile, 1, s.bb ? (cuuint32_t)s.bb : 1u};
-        const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)ks.n, (cuuint64_t)(ks.sets * pb.kv_heads)};
-        const cuuint64_t kst[2] = {(cuuint64_t)D * 2, (cuuint64_t)ks.n * D * 2};
-        const cuuint32_t kb[3] = {64, kTile, 1};
-        if (!make_map(&maps.q[k], q, 4, qd, qs, qb) || !make_map(&maps.k[k], ks.k, 3, kd, kst, kb) ||
-            !make_map(&maps.v[k], ks.v, 3, kd, kst, kb))
-            return cudaErrorInvalidValue;
-    }
-    auto kern = dense_fwd_kernel<D>;
+    const FwdSet &s = p.plan.s;
+    const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)pb.rows, (cuuint64_t)pb.kv_heads, (cuuint64_t)pb.batch};
+    const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)pb.rows * D * 2, (cuuint64_t)pb.kv_heads * pb.rows * D * 2};
+    const cuuint32_t qb[4] = {64, s.bb ? (cuuint32_t)pb.rows : (cuuint32_t)kTile, 1, s.bb ? (cuuint32_t)s.bb : 1u};
+    const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)ks.n, (cuuint64_t)(ks.sets * pb.kv_heads)};
+    const cuuint64_t kst[2] = {(cuuint64_t)D * 2, (cuuint64_t)ks.n * D * 2};
+    const cuuint32_t kb[3] = {64, kTile, 1};
+    if (!make_map(&maps.q, q, 4, qd, qs, qb) || !make_map(&maps.k, ks.k, 3, kd, kst, kb) ||
+        !make_map(&maps.v, ks.v, 3, kd, kst, kb))
+        return cudaErrorInvalidValue;
+    auto kern = dense_fwd_kernel<D, FEW>;
     const size_t smem = sizeof(Shared<D>) + 1024;
     static_assert(sizeof(Shared<D>) + 1024 <= 232448, "shared memory");
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -831,70 +944,69 @@ cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet *sets, Fw
     if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
     if (fa.numRegs * NTHREADS < kRegsNeeded || fa.maxThreadsPerBlock < NTHREADS) return cudaErrorInvalidConfiguration;
     kern<<<p.plan.ctas, NTHREADS, smem, stream>>>(maps, p);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if (p.plan.nsets == 2)
-        join_two_kernel<D><<<(unsigned)((p.all_rows + 7) / 8), 256, 0, stream>>>(p);
-    else if (p.plan.stream && p.plan.ctas > 1)
-        join_one_kernel<D><<<dim3(p.plan.ctas - 1, p.plan.s[0].few ? kFewRows / 8 : 2 * kTile / 8), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+template <int D> cudaError_t run(const DenseProblem &pb, const void *q, const KeySet *sets, int nsets, FwdParams *p, cudaStream_t stream) {
+    for (int k = 0; k < nsets; ++k) {
+        const cudaError_t e = p[k].plan.s.few ? launch<D, true>(pb, q, sets[k], p[k], stream)
+                                              : launch<D, false>(pb, q, sets[k], p[k], stream);
+        if (e != cudaSuccess) return e;
+    }
+    if (nsets == 2) {
+        join_sets_kernel<D><<<(unsigned)((p[0].all_rows + 7) / 8), 256, 0, stream>>>(p[0], p[1]);
+    } else if (p[0].cuts) {
+        const int each = p[0].plan.s.few ? 1 : kJoinRows, rows = p[0].plan.s.few ? kFewRows : 2 * kTile;
+        join_cut_kernel<D><<<dim3(p[0].plan.ctas, rows / (8 * each)), 256, 0, stream>>>(p[0], each);
+    }
     return cudaGetLastError();
 }
 
 }  // namespace
 
-FwdPlan make_fwd_plan(const DenseProblem &p, const KeySet *sets, int nsets) {
+FwdPlan make_fwd_plan(const DenseProblem &p, const KeySet &ks) {
     FwdPlan r{};
-    r.nsets = nsets;
     r.rows = p.rows;
     r.kv_heads = p.kv_heads;
     r.batch = p.batch;
-    int64_t units = 0, steps = 0, most = 0;
-    bool scan = true;
-    for (int k = 0; k < nsets; ++k) {
-        const KeySet &ks = sets[k];
-        FwdSet &s = r.s[k];
-        s.len = ks.len;
-        s.n = ks.n;
-        s.sets = ks.sets;
-        s.members = ks.members;
-        s.few = p.rows <= kFewRows && ks.members * p.rows <= kFewRows;
-        if (p.rows <= kTile) {
-            const int64_t fit = kTile / p.rows;
-            s.bb = (int32_t)(ks.members < fit ? ks.members : fit);
-            s.tpm = 0;
-            s.tiles = (ks.members + s.bb - 1) / s.bb;
-        } else {
-            s.bb = 0;
-            s.tpm = (int32_t)((p.rows + kTile - 1) / kTile);
-            s.tiles = ks.members * s.tpm;
-        }
-        s.pairs = (s.tiles + 1) / 2;
-        s.upz = p.kv_heads * s.pairs;
-        const int64_t t = (ks.n + kTile - 1) / kTile;
-        units += s.sets * s.upz;
-        steps += s.sets * s.upz * t;
-        most = t > most ? t : most;
-        scan = scan && (!ks.len || ks.sets <= 1024);
+    FwdSet &s = r.s;
+    s.len = ks.len;
+    s.n = ks.n;
+    s.sets = ks.sets;
+    s.members = ks.members;
+    s.few = p.rows <= kFewRows && ks.members * p.rows <= kFewRows;
+    if (p.rows <= kTile) {
+        const int64_t fit = kTile / p.rows;
+        s.bb = (int32_t)(ks.members < fit ? ks.members : fit);
+        s.tiles = (ks.members + s.bb - 1) / s.bb;
+    } else {
+        s.tpm = (int32_t)((p.rows + kTile - 1) / kTile);
+        s.tiles = ks.members * s.tpm;
     }
+    s.pairs = (s.tiles + 1) / 2;
+    s.upz = p.kv_heads * s.pairs;
+    const int64_t t = (ks.n + kTile - 1) / kTile, units = s.sets * s.upz;
     // Units of a few steps each, or very many of them, go whole to the CTAs: cutting would save less
-    // than the join costs.
-    r.stream = scan && most > 4 && units < 16 * kCtas;
-    const int64_t want = r.stream ? (steps + 1) / 2 : units;
+    // than the join costs. The scan of the lengths is a warp's work at a kernel's start.
+    r.stream = t > 4 && units < 16 * kCtas && (!ks.len || ks.sets <= 1024);
+    const int64_t want = r.stream ? (units * t + 1) / 2 : units;
     r.ctas = (int32_t)(want < kCtas ? want : kCtas);
     return r;
 }
 
-FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d) {
+FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d, bool two_sets) {
     FwdLayout L{};
     size_t o = 0;
     auto take = [&](size_t floats) { const size_t at = o; o += (floats + 63) / 64 * 64; return at; };
     const size_t all = (size_t)plan.batch * plan.kv_heads * plan.rows;
-    if (plan.stream && plan.ctas > 1) {
+    if (plan.stream) {
         L.part_o = take((size_t)plan.ctas * 4 * kTile * d);
         L.part_lse = take((size_t)plan.ctas * 4 * kTile);
+        L.cuts = take((size_t)plan.ctas * 4);
     }
-    if (plan.nsets == 2) {
-        L.whole_o = take(2 * all * d);
-        L.whole_lse = take(2 * all);
+    if (two_sets) {
+        L.whole_o = take(all * d);
+        L.whole_lse = take(all);
+        L.spans = take((size_t)plan.s.sets * plan.s.upz * 2);
     }
     L.total = o;
     return L;
@@ -902,19 +1014,28 @@ FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d) {
 
 cudaError_t launch_dense_fwd(const DenseProblem &pb, const void *q, const KeySet *sets, int nsets, void *out, float *lse,
                              float *ws, uint32_t *status, cudaStream_t stream) {
-    FwdParams p{};
-    p.plan = make_fwd_plan(pb, sets, nsets);
-    const FwdLayout L = fwd_layout_of(p.plan, pb.d);
-    p.out = static_cast<__nv_bfloat16 *>(out);
-    p.lse = lse;
-    p.part_o = ws + L.part_o;
-    p.part_lse = ws + L.part_lse;
-    p.whole_o = nsets == 2 ? ws + L.whole_o : nullptr;
-    p.whole_lse = nsets == 2 ? ws + L.whole_lse : nullptr;
-    p.all_rows = pb.batch * pb.kv_heads * pb.rows;
-    p.scale_log2 = pb.scale * 1.4426950408889634f;
-    p.status = status;
-    return pb.d == 64 ? launch<64>(pb, q, sets, p, stream) : launch<128>(pb, q, sets, p, stream);
+    FwdParams p[2] = {};
+    for (int k = 0; k < nsets; ++k) {
+        FwdParams &x = p[k];
+        x.plan = make_fwd_plan(pb, sets[k]);
+        const FwdLayout L = fwd_layout_of(x.plan, pb.d, nsets == 2);
+        x.out = static_cast<__nv_bfloat16 *>(out);
+        x.lse = lse;
+        x.part_o = ws + L.part_o;
+        x.part_lse = ws + L.part_lse;
+        if (nsets == 2) {
+            x.whole_o = ws + L.whole_o;
+            x.whole_lse = ws + L.whole_lse;
+            x.spans = reinterpret_cast<int2 *>(ws + L.spans);
+        } else if (x.plan.stream) {
+            x.cuts = reinterpret_cast<Cut *>(ws + L.cuts);
+        }
+        x.all_rows = pb.batch * pb.kv_heads * pb.rows;
+        x.scale_log2 = pb.scale * 1.4426950408889634f;
+        x.status = status;
+        ws += L.total;
+    }
+    return pb.d == 64 ? run<64>(pb, q, sets, nsets, p, stream) : run<128>(pb, q, sets, nsets, p, stream);
 }
 
 }  // namespace bsa

@@ -24,12 +24,54 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// A value that is the same in all lanes, known to be so by the compiler too (all lanes take part).
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // Contiguous bytes (16-byte aligned, a multiple of 16) of global memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
+}
+
+// Waits for this thread's loads from tensor memory. The loaded values pass through the wait, so that
+// nothing that uses them can be moved ahead of it.
+__device__ __forceinline__ void tmem_wait_ld_of(float (&x)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]),
+          "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]), "+f"(x[16]),
+          "+f"(x[17]), "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]), "+f"(x[24]),
+          "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]), "+f"(x[30]), "+f"(x[31])
+        :
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld_of(float (&x)[64]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+        : "+f"(x[0]), "+f"(x[1]), "+f"(x[2]), "+f"(x[3]), "+f"(x[4]), "+f"(x[5]), "+f"(x[6]), "+f"(x[7]), "+f"(x[8]),
+          "+f"(x[9]), "+f"(x[10]), "+f"(x[11]), "+f"(x[12]), "+f"(x[13]), "+f"(x[14]), "+f"(x[15]), "+f"(x[16]),
+          "+f"(x[17]), "+f"(x[18]), "+f"(x[19]), "+f"(x[20]), "+f"(x[21]), "+f"(x[22]), "+f"(x[23]), "+f"(x[24]),
+          "+f"(x[25]), "+f"(x[26]), "+f"(x[27]), "+f"(x[28]), "+f"(x[29]), "+f"(x[30]), "+f"(x[31]), "+f"(x[32]),
+          "+f"(x[33]), "+f"(x[34]), "+f"(x[35]), "+f"(x[36]), "+f"(x[37]), "+f"(x[38]), "+f"(x[39]), "+f"(x[40]),
+          "+f"(x[41]), "+f"(x[42]), "+f"(x[43]), "+f"(x[44]), "+f"(x[45]), "+f"(x[46]), "+f"(x[47]), "+f"(x[48]),
+          "+f"(x[49]), "+f"(x[50]), "+f"(x[51]), "+f"(x[52]), "+f"(x[53]), "+f"(x[54]), "+f"(x[55]), "+f"(x[56]),
+          "+f"(x[57]), "+f"(x[58]), "+f"(x[59]), "+f"(x[60]), "+f"(x[61]), "+f"(x[62]), "+f"(x[63])
+        :
+        : "memory");
+}
+// Bounded wait (2 s, as wait_bar) that does not read the global timer, which costs more than most waits
+// last, before it has been suspended a few times.
+__device__ __forceinline__ bool wait_soon(uint64_t *b, uint32_t parity, volatile int *abort_flag, uint32_t *status) {
+    if (mbar_try_wait(b, parity)) return true;
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+        if (mbar_try_wait_sleep(b, parity, kSleepNs)) return true;
+    return wait_bar(b, parity, abort_flag, status);
+}
+// One arrival for a whole warp, after all its lanes (32 arrivals at one address would queue up).
+__device__ __forceinline__ void warp_arrive(uint64_t *bar, int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
 }
 
 // D (TMEM) (+)= A·B with A (K-major bf16 pairs, the lanes of D) read from tensor memory.
@@ -48,6 +90,30 @@ constexpr uint32_t idesc_of(int n, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// 2^x of two values on the FMA pipe, x <= about 2^8: x = n + f with n = round(x), f in [-1/2, 1/2]; 2^f
+// by the degree-3 minimax polynomial that the block-sparse kernel's route uses too (relative error
+// 7.5e-5, an eighth of a bf16 rounding's mean), and n added to the exponent. Below -125 it gives
+// 2^-125, where a softmax weight is nothing.
+__device__ __forceinline__ float2 exp2_fma2(float2 x) {
+    x.x = fmaxf(x.x, -125.f);
+    x.y = fmaxf(x.y, -125.f);
+    const float2 t = __fadd2_rn(x, make_float2(0x1.8p23f, 0x1.8p23f));           // low bits: n
+    const float2 f = __fadd2_rn(x, __fadd2_rn(make_float2(0x1.8p23f, 0x1.8p23f), make_float2(-t.x, -t.y)));
+    float2 p = __ffma2_rn(f, make_float2(0x1.c3f76p-5f, 0x1.c3f76p-5f), make_float2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
+    p = __ffma2_rn(p, f, make_float2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
+    p = __ffma2_rn(p, f, make_float2(0x1.fff692p-1f, 0x1.fff692p-1f));
+    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
+                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+}
+// 32 lanes x 16 columns: thread t of the warp gets TMEM lane (base + t).
+__device__ __forceinline__ void tmem_ld16w(uint32_t taddr, uint32_t *u) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+          "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
+        : "r"(taddr));
+}
 // 32 lanes x 16 columns: thread t of the warp writes TMEM lane (base + t).
 __device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t *u) {
     asm volatile(
