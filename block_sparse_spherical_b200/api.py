@@ -231,6 +231,12 @@ class LatLonToHealpix:
         return out
 
 
+def _raw_stream(index: int) -> int:
+    """The current stream of a device (the cheap way, where this torch has it: it is asked in every call)."""
+    get = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return get(index) if get is not None else torch.cuda.current_stream(index).cuda_stream
+
+
 class _DenseLayer:
     """What the layers of fixed sizes below share: their device, status word and calls on it.
 
@@ -248,27 +254,38 @@ class _DenseLayer:
         self.device = self.status.device
         if not self.status.is_cuda:
             raise ValueError(f"the layer needs a CUDA device, got {device}")
+        self._status_ptr = self.status.data_ptr()
         self._code = abi.BSA_BF16 if dtype == torch.bfloat16 else abi.BSA_F32
 
-    def _take(self, t, name, shape, dtype=None):
-        _require(t, name, self.dtype if dtype is None else dtype, shape)
-        if t.device != self.device:
-            raise ValueError(f"{name} must be on {self.device}, got {t.device}")
+    def _take(self, t, name, shape, dtype=None) -> int:
+        """The address of a tensor of the layer's device, of this shape and dtype, contiguous."""
+        dtype = self.dtype if dtype is None else dtype
+        try:                                # what a good tensor passes at once
+            if t.shape == shape and t.dtype is dtype and t.device == self.device and t.is_contiguous():
+                return t.data_ptr()
+        except AttributeError:
+            pass
+        _require(t, name, dtype, shape)
+        raise ValueError(f"{name} must be on {self.device}, got {t.device}")
 
     def _lengths(self, t, name, count):
-        if t is not None:
-            self._take(t, name, (count,), torch.int32)
+        return None if t is None else self._take(t, name, (count,), torch.int32)
 
-    def _workspace(self, nbytes):
-        return torch.empty(nbytes, dtype=torch.uint8, device=self.device) if nbytes else None
+    def _output(self, t, name, shape, like):
+        """An output of the caller's, or a new one like an input that was checked, and its address."""
+        if t is None:
+            t = torch.empty_like(like)
+            return t, t.data_ptr()
+        return t, self._take(t, name, shape)
 
-    def _on_device(self, call, *args):
-        stream = torch.cuda.current_stream(self.device).cuda_stream
-        if torch.cuda.current_device() == self.device.index:
-            call(*args, self.status, stream)
-        else:
+    def _run(self, call, args, workspace_bytes):
+        """One call of the C ABI on the layer's device and its current stream, with a workspace."""
+        if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
-                call(*args, self.status, stream)
+                return self._run(call, args, workspace_bytes)
+        ws = torch.empty(workspace_bytes, dtype=torch.uint8, device=self.device) if workspace_bytes else None
+        call(self.cfg, *args, None if ws is None else ws.data_ptr(), workspace_bytes, self._status_ptr,
+             _raw_stream(self.device.index))
 
     def check_status(self) -> int:
         """Synchronise and return the kernels' status code (0 = OK); resets it."""
@@ -294,16 +311,11 @@ class CrossAttention(_DenseLayer):
         self.kv_shape = (batch, self.kv_heads, n_k, head_dim)
 
     def _forward(self, q, k, v, key_len, out, lse):
-        self._take(q, "q", self.shape)
-        self._take(k, "k", self.kv_shape)
-        self._take(v, "v", self.kv_shape)
-        self._lengths(key_len, "key_len", self.batch)
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            self._take(out, "out", self.shape)
-        self._on_device(abi.bsa_cross_attention, self.cfg, q, k, v, key_len, out, lse,
-                        self._workspace(self.workspace_bytes), self.workspace_bytes)
+        args = (self._take(q, "q", self.shape), self._take(k, "k", self.kv_shape), self._take(v, "v", self.kv_shape),
+                self._lengths(key_len, "key_len", self.batch))
+        out, address = self._output(out, "out", self.shape, q)
+        self._run(abi.bsa_cross_attention, (*args, address, None if lse is None else lse.data_ptr()),
+                  self.workspace_bytes)
         return out
 
     def __call__(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
@@ -335,17 +347,13 @@ class CrossAttentionTrain(CrossAttention):
         """Gradients (dq, dk, dv) of the last forward() for dL/dout = dout."""
         if self._saved is None:
             raise RuntimeError("backward() needs a forward() first")
-        q, k, v, key_len, out, lse = self._saved
-        self._take(dout, "dout", self.shape)
-        if grads is None:
-            grads = (torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
-        else:
-            for t, name, shape in zip(grads, ("dq", "dk", "dv"), (self.shape, self.kv_shape, self.kv_shape)):
-                self._take(t, name, shape)
-        dq, dk, dv = grads
-        self._on_device(abi.bsa_cross_attention_backward, self.cfg, q, k, v, key_len, out, lse, dout, dq, dk, dv,
-                        self._workspace(self.bwd_workspace_bytes), self.bwd_workspace_bytes)
-        return dq, dk, dv
+        saved = self._saved
+        outs = [self._output(t, name, shape, like) for t, name, shape, like in
+                zip(grads or (None,) * 3, ("dq", "dk", "dv"), (self.shape, self.kv_shape, self.kv_shape), saved)]
+        args = (*(None if t is None else t.data_ptr() for t in saved), self._take(dout, "dout", self.shape),
+                *(address for _, address in outs))
+        self._run(abi.bsa_cross_attention_backward, args, self.bwd_workspace_bytes)
+        return tuple(t for t, _ in outs)
 
 
 class PrefixAttention(_DenseLayer):
@@ -372,19 +380,12 @@ class PrefixAttention(_DenseLayer):
 
     def __call__(self, q, k_prefix, v_prefix, k_own, v_own, prefix_len=None, own_len=None,
                  out=None) -> torch.Tensor:
-        self._take(q, "q", self.shape)
-        self._take(k_prefix, "k_prefix", self.prefix_shape)
-        self._take(v_prefix, "v_prefix", self.prefix_shape)
-        self._take(k_own, "k_own", self.own_shape)
-        self._take(v_own, "v_own", self.own_shape)
-        self._lengths(prefix_len, "prefix_len", self.groups)
-        self._lengths(own_len, "own_len", self.batch)
-        if out is None:
-            out = torch.empty_like(q)
-        else:
-            self._take(out, "out", self.shape)
-        self._on_device(abi.bsa_prefix_attention, self.cfg, q, k_prefix, v_prefix, prefix_len, k_own, v_own, own_len,
-                        out, self._workspace(self.workspace_bytes), self.workspace_bytes)
+        args = (self._take(q, "q", self.shape), self._take(k_prefix, "k_prefix", self.prefix_shape),
+                self._take(v_prefix, "v_prefix", self.prefix_shape),
+                self._lengths(prefix_len, "prefix_len", self.groups), self._take(k_own, "k_own", self.own_shape),
+                self._take(v_own, "v_own", self.own_shape), self._lengths(own_len, "own_len", self.batch))
+        out, address = self._output(out, "out", self.shape, q)
+        self._run(abi.bsa_prefix_attention, (*args, address), self.workspace_bytes)
         return out
 
 

@@ -990,16 +990,6 @@ bool row_map(CUtensorMap *m, const void *base, int64_t d, int64_t rows, int64_t 
     return make_map(m, base, 3, dims, strides, b);
 }
 
-template <typename K>
-cudaError_t prepare(K kern, size_t smem) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-    return fa.numRegs * NTHREADS < kRegsNeeded || fa.maxThreadsPerBlock < NTHREADS ? cudaErrorInvalidConfiguration
-                                                                                  : cudaSuccess;
-}
-
 template <int D>
 cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, const void *out, const float *lse,
                    const void *dout, const BwdPlans &plans, BwdParams key, float *stat, float *qry_part,
@@ -1016,8 +1006,8 @@ cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, cons
     qry.part = qry_part;
     const size_t ksm = sizeof(KeyShared<D>) + 1024, qsm = sizeof(QryShared<D>) + 1024;
     static_assert(sizeof(KeyShared<D>) + 1024 <= 232448 && sizeof(QryShared<D>) + 1024 <= 232448, "shared memory");
-    cudaError_t e = prepare(bwd_key_kernel<D>, ksm);
-    if (e == cudaSuccess) e = prepare(bwd_qry_kernel<D>, qsm);
+    cudaError_t e = kernel_ready<bwd_key_kernel<D>>(ksm, NTHREADS, kRegsNeeded);
+    if (e == cudaSuccess) e = kernel_ready<bwd_qry_kernel<D>>(qsm, NTHREADS, kRegsNeeded);
     if (e != cudaSuccess) return e;
     const int64_t stat_blocks = (slabs * plans.qtiles * kSub + 256 / (D / 8) - 1) / (256 / (D / 8));
     bwd_stat_kernel<D><<<(unsigned)(stat_blocks < 8 * kCtas ? stat_blocks : 8 * kCtas), 256, 0, stream>>>(

@@ -934,16 +934,11 @@ template <int D, bool FEW> cudaError_t launch(const DenseProblem &pb, const void
     if (!make_map(&maps.q, q, 4, qd, qs, qb) || !make_map(&maps.k, ks.k, 3, kd, kst, kb) ||
         !make_map(&maps.v, ks.v, 3, kd, kst, kb))
         return cudaErrorInvalidValue;
-    auto kern = dense_fwd_kernel<D, FEW>;
     const size_t smem = sizeof(Shared<D>) + 1024;
     static_assert(sizeof(Shared<D>) + 1024 <= 232448, "shared memory");
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = kernel_ready<dense_fwd_kernel<D, FEW>>(smem, NTHREADS, kRegsNeeded);
     if (e != cudaSuccess) return e;
-    // setmaxnreg.inc would wait forever for registers that the CTA was not launched with
-    cudaFuncAttributes fa;
-    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
-    if (fa.numRegs * NTHREADS < kRegsNeeded || fa.maxThreadsPerBlock < NTHREADS) return cudaErrorInvalidConfiguration;
-    kern<<<p.plan.ctas, NTHREADS, smem, stream>>>(maps, p);
+    dense_fwd_kernel<D, FEW><<<p.plan.ctas, NTHREADS, smem, stream>>>(maps, p);
     return cudaGetLastError();
 }
 template <int D> cudaError_t run(const DenseProblem &pb, const void *q, const KeySet *sets, int nsets, FwdParams *p, cudaStream_t stream) {

@@ -3,6 +3,8 @@
 // host side of their tensor maps.
 #pragma once
 
+#include <atomic>
+
 #include "tc_common.cuh"
 
 namespace bsa {
@@ -134,6 +136,25 @@ inline bool make_map(CUtensorMap *map, const void *base, int rank, const cuuint6
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void *>(base), dims, strides, box, one,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Sets a kernel up for its dynamic shared memory, once a device: later calls on the same device cost a
+// look at a bit. Also refuses a kernel whose register split (setmaxnreg.inc would wait forever for
+// registers that a CTA was not launched with) does not fit what it was compiled to.
+template <auto KERNEL>
+inline cudaError_t kernel_ready(size_t smem, int threads, int regs_needed) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, KERNEL)) != cudaSuccess) return e;
+    if (fa.numRegs * threads < regs_needed || fa.maxThreadsPerBlock < threads) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 }  // namespace tc
