@@ -94,18 +94,18 @@ constexpr uint32_t idesc_of(int n, bool b_mn) {
 
 // 2^x of two values on the FMA pipe, x <= about 2^8: x = n + f with n = round(x), f in [-1/2, 1/2]; 2^f
 // by the degree-3 minimax polynomial that the block-sparse kernel's route uses too (relative error
-// 7.5e-5, an eighth of a bf16 rounding's mean), and n added to the exponent. Below -125 it gives
-// 2^-125, where a softmax weight is nothing.
+// 7.5e-5, a twentieth of a bf16 rounding's mean), times 2^n. Below -125 it gives 2^-125, where a
+// softmax weight is nothing. NaN gives NaN.
 __device__ __forceinline__ float2 exp2_fma2(float2 x) {
-    x.x = fmaxf(x.x, -125.f);
-    x.y = fmaxf(x.y, -125.f);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-125.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-125.f));
     const float2 t = __fadd2_rn(x, make_float2(0x1.8p23f, 0x1.8p23f));           // low bits: n
     const float2 f = __fadd2_rn(x, __fadd2_rn(make_float2(0x1.8p23f, 0x1.8p23f), make_float2(-t.x, -t.y)));
     float2 p = __ffma2_rn(f, make_float2(0x1.c3f76p-5f, 0x1.c3f76p-5f), make_float2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
     p = __ffma2_rn(p, f, make_float2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
     p = __ffma2_rn(p, f, make_float2(0x1.fff692p-1f, 0x1.fff692p-1f));
-    return make_float2(__uint_as_float(__float_as_uint(p.x) + (__float_as_uint(t.x) << 23)),
-                       __uint_as_float(__float_as_uint(p.y) + (__float_as_uint(t.y) << 23)));
+    return __fmul2_rn(p, make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
+                                     __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u)));
 }
 // 32 lanes x 16 columns: thread t of the warp gets TMEM lane (base + t).
 __device__ __forceinline__ void tmem_ld16w(uint32_t taddr, uint32_t *u) {

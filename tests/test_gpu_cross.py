@@ -119,6 +119,20 @@ def test_nan_in_a_state_that_counts_stays_in_its_rows():
     assert torch.isnan(out[1, 0]).all() and torch.isfinite(out[0]).all() and torch.isfinite(out[1, 1]).all()
 
 
+@pytest.mark.parametrize("row", range(0, 64, 7))
+def test_nan_in_a_key_or_query_reaches_all_that_it_meets(row):
+    q, k, v, g = inputs(1, 2, 2, 70, 150, 64, seed=17)
+    k[0, 0, row] = float("nan")
+    q[0, 1, row] = float("nan")
+    layer = api.CrossAttentionTrain(1, 2, 70, 150, 64)
+    out = layer(q, k, v)
+    dq, dk, dv = layer.backward(g)
+    assert torch.isnan(out[0, 0]).all() and torch.isnan(out[0, 1, row]).all()
+    rest = [i for i in range(70) if i != row]
+    assert torch.isfinite(out[0, 1, rest]).all() and torch.isfinite(dq[0, 1, rest]).all()
+    assert torch.isnan(dq[0, 0]).all() and torch.isnan(dk[0]).all() and torch.isnan(dv[0]).all()
+
+
 def test_lengths_outside_the_buffer_are_clamped_and_flagged():
     q, k, v, g = inputs(2, 2, 2, 40, 200, 64, seed=8)
     layer = api.CrossAttentionTrain(2, 2, 40, 200, 64)
