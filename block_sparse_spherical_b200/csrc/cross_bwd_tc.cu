@@ -15,17 +15,18 @@
 //   KEY  (dk, dv): unit = keys, A0 = K, A1 = V; step = query rows, B0 = Q, B1 = dO;
 //   !KEY (dq):     unit = query rows, A0 = Q, A1 = dO; step = keys, B0 = K, B1 = V.
 // S = A0·B0ᵀ and dP = A1·B1ᵀ (tcgen05.mma, M = N = 128) go to tensor memory, where thread
-// (w, row) of 256 takes its unit row's columns 64w..64w+63; P (KEY only) and dS return there as
+// (w, row) of 512 takes its unit row's columns 32w..32w+31; P (KEY only) and dS return there as
 // bf16 pairs and are the A operands of acc0 += P·B1 (dv) and acc1 += dS·B0 (dk, dq), so
 // nothing passes through shared memory. S and dP have barriers of their own, and so have P and
 // dS: exponentials run while dP is formed, P·B1 while dS is computed, and S of the next step
 // as soon as this one's is read (where P has columns of its own) or its P used up (KEY,
 // D = 128, where tensor memory holds no more).
 //
-// One persistent CTA per SM, 384 threads: warp 0 copies, warp 1 issues S and dP, warp 2 the
+// One persistent CTA per SM, 640 threads: warp 0 copies, warp 1 issues S and dP, warp 2 the
 // gradients' products (one thread issues a tcgen05 instruction about every 60 clocks: with steps of 64
 // columns and twice the instructions, their issue set the pace, 1,300 clocks for 64 columns at
-// D = 64), warp 3 finds the units and hands them out, warps 4-11 the softmax.
+// D = 64), warp 3 finds the units and hands them out, warps 4-19 the softmax (with eight warps, two
+// a scheduler, a step's chain of waits, loads and stores took 1,900 clocks beside the exponentials).
 //
 // Tensor memory: S 0..127, dP 128..255. KEY, D = 64: P 256, dS 320 (64 columns each), dv 384, dk 448.
 // KEY, D = 128: P and dS in the place of the thread's own S and dP columns, dv 256, dk 384.
@@ -49,10 +50,11 @@ namespace {
 
 using namespace tc;
 
-constexpr int NTHREADS = 384;
-constexpr int kCtrlRegs = 72, kSoftRegs = 216;
-constexpr int kRegsNeeded = 128 * kCtrlRegs + 256 * kSoftRegs;
-static_assert(kRegsNeeded <= 65536, "register split");
+constexpr int kSoftWarps = 16;              // of the softmax: thread (w, row) has columns 32w.. of a step
+constexpr int NTHREADS = 128 + 32 * kSoftWarps;
+constexpr int kCtrlRegs = 56, kSoftRegs = 104;
+constexpr int kRegsNeeded = 128 * kCtrlRegs + 32 * kSoftWarps * kSoftRegs;
+static_assert(kRegsNeeded <= 65536 / NTHREADS / 8 * 8 * NTHREADS, "register split");
 constexpr int kStat = 2 * kTile;            // floats of a query tile's statistics: lse·log2 e, then D
 
 struct BwdParams {
@@ -131,13 +133,13 @@ struct Chunk {
     int64_t slab;
 };
 constexpr int kChunks = 4;
-constexpr int kReaders = 11;                // warps that read a chunk: copy, 2 MMA, 8 softmax
+constexpr int kReaders = 3 + kSoftWarps;     // warps that read a chunk: copy, 2 MMA, softmax
 template <int D> struct alignas(1024) Shared {
     uint8_t a0[Cfg<D>::UB][Cfg<D>::TILE], a1[Cfg<D>::UB][Cfg<D>::TILE];
     uint8_t b0[Cfg<D>::STAGES][Cfg<D>::TILE], b1[Cfg<D>::STAGES][Cfg<D>::TILE];
     float stat[Cfg<D>::STAGES][kStat];
     uint64_t u_full[2], u_empty[2], st_full[4], st_empty[4], tail;
-    uint64_t s_full, dp_full, s_free, dp_free, p_full, ds_full, v_done, k_done, acc_full, acc_free, drain[2];
+    uint64_t s_full, dp_full, s_free, p_full, ds_full, v_done, k_done, acc_full, acc_free, drain[2];
     uint64_t ch_full[kChunks], ch_empty[kChunks];
     Chunk ch[kChunks];
     uint32_t tmem_base;
@@ -321,15 +323,15 @@ __device__ void copy_role(const BwdParams &p, const BwdMaps &maps, Shared<D> &sh
 }
 
 constexpr uint32_t kColS = 0, kColDp = 128;
-// P and dS of column half w
-template <int D, bool KEY> __device__ __forceinline__ uint32_t col_p(int w) { return D == 64 ? 256u + 32u * w : 64u * w; }
+// P and dS take the place of S and dP
+template <int D, bool KEY> constexpr bool kInPlace = KEY && D == 128;
+// P and dS of columns 32w..32w+31 of a step
+template <int D, bool KEY> __device__ __forceinline__ uint32_t col_p(int w) { return kInPlace<D, KEY> ? 32u * w : 256u + 16u * w; }
 template <int D, bool KEY> __device__ __forceinline__ uint32_t col_ds(int w) {
-    return !KEY ? 256u + 32u * w : (D == 64 ? 320u + 32u * w : 128u + 64u * w);
+    return kInPlace<D, KEY> ? 128u + 32u * w : (KEY ? 320u : 256u) + 16u * w;
 }
 template <int D, bool KEY> constexpr uint32_t kColV = D == 64 ? 384u : 256u;
 template <int D, bool KEY> constexpr uint32_t kColK = !KEY ? 320u : (D == 64 ? 448u : 384u);
-// P and dS take the place of S and dP
-template <int D, bool KEY> constexpr bool kInPlace = KEY && D == 128;
 
 // S and dP of every step.
 template <int D, bool KEY>
@@ -370,7 +372,8 @@ __device__ void score_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int
                 commit(&sh.s_full);
             }
             __syncwarp();
-            if (g > 0 && !(ok = wait_w(kInPlace<D, KEY> ? &sh.k_done : &sh.dp_free, (g - 1) & 1))) break;
+            // those of dP: read, as dS of the step before is written, or (dS in their place) used up
+            if (g > 0 && !(ok = wait_w(kInPlace<D, KEY> ? &sh.k_done : &sh.ds_full, (g - 1) & 1))) break;
             fence_after();
             if (leader) {
                 product(kColDp, a1 + (uint64_t)(ub * (C::TILE >> 4)), b1 + (uint64_t)(st * (C::TILE >> 4)));
@@ -397,12 +400,13 @@ __device__ void grad_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int 
         return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     const uint64_t b0 = desc_mnmajor_sw128(sh.b0[0], kTile * 128), b1 = desc_mnmajor_sw128(sh.b1[0], kTile * 128);
-    auto product = [&](uint32_t acc, uint32_t a_lo, uint32_t a_hi, uint64_t b, bool first) __attribute__((always_inline)) {
+    auto product = [&](uint32_t acc, uint32_t a, uint32_t a_step, uint64_t b, bool first) __attribute__((always_inline)) {
 #pragma unroll
         for (int kk = 0; kk < kTile / 16; ++kk)        // blocks of 16 columns of the step
-            mma_ts(tmem + acc, tmem + (kk < 4 ? a_lo : a_hi) + 8u * (kk & 3), b + 128 * kk, idesc_of(D, true),
+            mma_ts(tmem + acc, tmem + a + a_step * (kk >> 1) + 8u * (kk & 1), b + 128 * kk, idesc_of(D, true),
                    (first && kk == 0) ? 0u : 1u);
     };
+    constexpr uint32_t STEP = kInPlace<D, KEY> ? 32 : 16;
     uint32_t u = 0, g = 0;
     bool ok = true;
     const Chunk *cp;
@@ -418,15 +422,15 @@ __device__ void grad_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int 
                 if (!(ok = wait_w(&sh.p_full, g & 1))) break;
                 fence_after();
                 if (leader) {
-                    product(kColV<D, KEY>, col_p<D, KEY>(0), col_p<D, KEY>(1), b1 + (uint64_t)(st * (C::TILE >> 4)), t == 0);
-                    commit(&sh.v_done);
+                    product(kColV<D, KEY>, col_p<D, KEY>(0), STEP, b1 + (uint64_t)(st * (C::TILE >> 4)), t == 0);
+                    if (kInPlace<D, KEY>) commit(&sh.v_done);
                 }
                 __syncwarp();
             }
             if (!(ok = wait_w(&sh.ds_full, g & 1))) break;
             fence_after();
             if (leader) {
-                product(kColK<D, KEY>, col_ds<D, KEY>(0), col_ds<D, KEY>(1), b0 + (uint64_t)(st * (C::TILE >> 4)), t == 0);
+                product(kColK<D, KEY>, col_ds<D, KEY>(0), STEP, b0 + (uint64_t)(st * (C::TILE >> 4)), t == 0);
                 commit(&sh.k_done);
                 commit(&sh.st_empty[st]);
                 if (t + 1 == nt) commit(&sh.acc_full);
@@ -457,7 +461,10 @@ __device__ __forceinline__ void grad32(__nv_bfloat16 *dst16, float *dst32, const
 
 
 // Of 16 pairs of exponentials, how many take the polynomial on the FMA pipe.
-constexpr int kPoly = 4;
+#ifndef KPOLYB
+#define KPOLYB 4
+#endif
+constexpr int kPoly = KPOLYB;
 
 template <int D, bool KEY>
 __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int w, int wq, int lane) {
@@ -489,19 +496,18 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
             // complete) makes the copied values visible to it
             if (KEY && !(ok = wait_all(&sh.st_full[st], (g / C::STAGES) & 1))) break;
             fence_after();
-            float x[64];
-            tmem_ld32(tw + kColS + 64u * w, x);
-            tmem_ld32(tw + kColS + 64u * w + 32, x + 32);
+            float x[32];
+            tmem_ld32(tw + kColS + 32u * w, x);
             tmem_wait_ld_of(x);
             if constexpr (!IN_PLACE) {
                 fence_before();
                 warp_arrive(&sh.s_free, lane);
             }
             // p = 2^(c·log2 e·s - lse·log2 e), in place, 16 at a time
-            const float4 *ls4 = reinterpret_cast<const float4 *>(sh.stat[st] + 64 * w);
-            const float4 *dd4 = reinterpret_cast<const float4 *>(sh.stat[st] + kTile + 64 * w);
+            const float4 *ls4 = reinterpret_cast<const float4 *>(sh.stat[st] + 32 * w);
+            const float4 *dd4 = reinterpret_cast<const float4 *>(sh.stat[st] + kTile + 32 * w);
 #pragma unroll
-            for (int h = 0; h < 4; ++h) {
+            for (int h = 0; h < 2; ++h) {
                 float2 e2[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -519,62 +525,53 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
                     x[16 * h + 2 * e + 1] = e2[e].y;
                 }
             }
-            const int valid = cols - t * kTile - 64 * w;
-            if (KEY ? !counts : valid < 64) {
+            const int valid = cols - t * kTile - 32 * w;
+            if (KEY ? !counts : valid < 32) {
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
+                for (int e = 0; e < 32; ++e)
                     if (KEY || e >= valid) x[e] = 0.f;
             }
+            // the columns that P and dS take are free: the gradients' products of the step before have read them
+            // (in place: before this S and this dP began)
+            if (KEY && !IN_PLACE && g > 0 && !(ok = wait_all(&sh.k_done, (g - 1) & 1))) break;
             if constexpr (KEY) {
-                // P's columns: read by the P·B1 of the step before, or this thread's own S
-                if (!IN_PLACE && g > 0 && !(ok = wait_all(&sh.v_done, (g - 1) & 1))) break;
                 fence_after();
+                uint32_t pk[16];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(x[32 * h + 2 * e], x[32 * h + 2 * e + 1]);
-                    tmem_st16w(tw + col_p<D, KEY>(w) + 16 * h, pk);
-                }
+                for (int e = 0; e < 16; ++e) pk[e] = pack_bf16x2(x[2 * e], x[2 * e + 1]);
+                tmem_st16w(tw + col_p<D, KEY>(w), pk);
                 tmem_wait_st();
                 fence_before();
                 warp_arrive(&sh.p_full, lane);
             }
             if (!(ok = wait_all(&sh.dp_full, g & 1))) break;
             fence_after();
-            uint32_t ds[32];
+            float d[32];
+            uint32_t ds[16];
+            tmem_ld32(tw + kColDp + 32u * w, d);
+            tmem_wait_ld_of(d);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float d[32];
-                tmem_ld32(tw + kColDp + 64u * w + 32u * h, d);
-                tmem_wait_ld_of(d);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float4 d4 = KEY ? dd4[8 * h + e] : make_float4(dt, dt, dt, dt);
-                    const int c = 32 * h + 4 * e;
-                    float2 a = __fmul2_rn(make_float2(x[c], x[c + 1]),
-                                          __fadd2_rn(make_float2(d[4 * e], d[4 * e + 1]), make_float2(-d4.x, -d4.y)));
-                    float2 b = __fmul2_rn(make_float2(x[c + 2], x[c + 3]),
-                                          __fadd2_rn(make_float2(d[4 * e + 2], d[4 * e + 3]), make_float2(-d4.z, -d4.w)));
-                    ds[16 * h + 2 * e] = pack_bf16x2(a.x, a.y);
-                    ds[16 * h + 2 * e + 1] = pack_bf16x2(b.x, b.y);
-                }
-            }
-            if constexpr (!IN_PLACE) {
-                fence_before();
-                warp_arrive(&sh.dp_free, lane);
+            for (int e = 0; e < 8; ++e) {
+                const float4 d4 = KEY ? dd4[e] : make_float4(dt, dt, dt, dt);
+                const int c = 4 * e;
+                const float2 a = __fmul2_rn(make_float2(x[c], x[c + 1]),
+                                            __fadd2_rn(make_float2(d[c], d[c + 1]), make_float2(-d4.x, -d4.y)));
+                const float2 b = __fmul2_rn(make_float2(x[c + 2], x[c + 3]),
+                                            __fadd2_rn(make_float2(d[c + 2], d[c + 3]), make_float2(-d4.z, -d4.w)));
+                ds[2 * e] = pack_bf16x2(a.x, a.y);
+                ds[2 * e + 1] = pack_bf16x2(b.x, b.y);
             }
             // what does not count is 0 whatever dP holds there (0·NaN)
-            if (KEY ? !counts : valid < 64) {
+            if (KEY ? !counts : valid < 32) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
+                for (int e = 0; e < 16; ++e) {
                     if (KEY || 2 * e >= valid) ds[e] = 0u;
                     else if (2 * e + 1 >= valid) ds[e] &= 0xffffu;
                 }
             }
-            if (!IN_PLACE && g > 0 && !(ok = wait_all(&sh.k_done, (g - 1) & 1))) break;
+            if (!KEY && g > 0 && !(ok = wait_all(&sh.k_done, (g - 1) & 1))) break;
             fence_after();
-            tmem_st32(tw + col_ds<D, KEY>(w), reinterpret_cast<const float *>(ds));
+            tmem_st16w(tw + col_ds<D, KEY>(w), ds);
             tmem_wait_st();
             fence_before();
             warp_arrive(&sh.ds_full, lane);
@@ -585,16 +582,17 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
             ++u;
             fence_after();
         }
-        // KEY: half 0 stores dv, half 1 dk (nothing where no key counts); !KEY: each half of dq's columns
-        const int c0 = KEY ? 0 : w * (D / 2), c1 = KEY ? D : (w + 1) * (D / 2);
-        const uint32_t col = KEY && w == 0 ? kColV<D, KEY> : kColK<D, KEY>;
+        // KEY: w = 0, 1 store dv's columns, 2, 3 dk's (nothing where no key counts); !KEY: dq's, D / 4 each
+        // (D = 64: w = 0, 1)
+        const int grad = KEY ? w >> 1 : 1, part = KEY ? w & 1 : w, wide = KEY ? D / 2 : 32;
+        const uint32_t col = grad == 0 ? kColV<D, KEY> : kColK<D, KEY>;
         const int64_t at = cp->slab * (KEY ? p.plan.s.n : p.plan.rows) + (int64_t)cp->tile * kTile + row;
         const int slot = cp->slot;
-        __nv_bfloat16 *d16 = slot >= 0 ? nullptr : (!KEY ? p.dq : w == 0 ? p.dv : p.dk) + at * D;
-        float *d32 = p.part + ((2 * (int64_t)blockIdx.x + max(slot, 0)) * kTile + row) * (KEY ? 2 * D : D) + (KEY ? w * D : 0);
+        __nv_bfloat16 *d16 = slot >= 0 ? nullptr : (!KEY ? p.dq : grad == 0 ? p.dv : p.dk) + at * D;
+        float *d32 = p.part + ((2 * (int64_t)blockIdx.x + max(slot, 0)) * kTile + row) * (KEY ? 2 * D : D) + (KEY ? grad * D : 0);
         if (!KEY || nt > 0) {
 #pragma unroll 1
-            for (int cc = c0; cc < c1; cc += 32) {
+            for (int cc = part * wide; cc < min(D, (part + 1) * wide); cc += 32) {
                 float y[32];
                 if (nt > 0) {
                     tmem_ld32(tw + col + cc, y);
@@ -603,7 +601,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
 #pragma unroll
                     for (int e = 0; e < 32; ++e) y[e] = 0.f;
                 }
-                if (counts) grad32(d16 ? d16 + cc : nullptr, d32 + cc, y, KEY && w == 0 ? 1.f : p.scale);
+                if (counts) grad32(d16 ? d16 + cc : nullptr, d32 + cc, y, grad == 0 ? 1.f : p.scale);
                 __syncwarp();
             }
         }
@@ -636,14 +634,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant_
         mbar_init(&sh.tail, 1);
         mbar_init(&sh.s_full, 1);
         mbar_init(&sh.dp_full, 1);
-        mbar_init(&sh.s_free, 8);
-        mbar_init(&sh.dp_free, 8);
-        mbar_init(&sh.p_full, 8);
-        mbar_init(&sh.ds_full, 8);
+        mbar_init(&sh.s_free, kSoftWarps);
+        mbar_init(&sh.p_full, kSoftWarps);
+        mbar_init(&sh.ds_full, kSoftWarps);
         mbar_init(&sh.v_done, 1);
         mbar_init(&sh.k_done, 1);
         mbar_init(&sh.acc_full, 1);
-        mbar_init(&sh.acc_free, 8);
+        mbar_init(&sh.acc_free, kSoftWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
