@@ -22,11 +22,11 @@
 // as soon as this one's is read (where P has columns of its own) or its P used up (KEY,
 // D = 128, where tensor memory holds no more).
 //
-// One persistent CTA per SM, 640 threads: warp 0 copies, warp 1 issues S and dP, warp 2 the
-// gradients' products (one thread issues a tcgen05 instruction about every 60 clocks: with steps of 64
-// columns and twice the instructions, their issue set the pace, 1,300 clocks for 64 columns at
-// D = 64), warp 3 finds the units and hands them out, warps 4-19 the softmax (with eight warps, two
-// a scheduler, a step's chain of waits, loads and stores took 1,900 clocks beside the exponentials).
+// One persistent CTA per SM, 640 threads: warp 0 finds the units, hands them out and copies their tiles,
+// warp 1 issues S and dP, warp 2 P·B1 (KEY), warp 3 dS·B0 (one thread issues a tcgen05 instruction
+// about every 60 clocks: one warp for all of them, or steps of 64 columns with twice the instructions,
+// and their issue sets the pace), warps 4-19 the softmax (with eight warps, two a scheduler, a step's
+// chain of waits, loads and stores took 1,900 clocks beside the exponentials).
 //
 // Tensor memory: S 0..127, dP 128..255. KEY, D = 64: P 256, dS 320 (64 columns each), dv 384, dk 448.
 // KEY, D = 128: P and dS in the place of the thread's own S and dP columns, dv 256, dk 384.
@@ -55,7 +55,7 @@ constexpr int NTHREADS = 128 + 32 * kSoftWarps;
 constexpr int kCtrlRegs = 56, kSoftRegs = 104;
 constexpr int kRegsNeeded = 128 * kCtrlRegs + 32 * kSoftWarps * kSoftRegs;
 static_assert(kRegsNeeded <= 65536 / NTHREADS / 8 * 8 * NTHREADS, "register split");
-constexpr int kStat = 2 * kTile;            // floats of a query tile's statistics: lse·log2 e, then D
+constexpr int kStat = 2 * kTile;            // floats of a query tile's statistics: -lse·log2 e, then -D
 
 struct BwdParams {
     FwdPlan plan;           // KEY: s.fixed query tiles a unit; !KEY: units are query tiles, steps key tiles
@@ -73,7 +73,8 @@ struct BwdMaps {
 
 // ---------------------------------------------------------------- statistics
 
-// Per query row lse·log2 e (+inf for rows without keys or behind the last: p = 0) and D = dout·out;
+// Per query row -lse·log2 e (-inf for rows without keys or behind the last: p = 0) and -D = -dout·out
+// (negated, since a packed add or fma has no negated operand);
 // and zeros for the gradients of keys behind a length. D/8 lanes a row, 16 bytes each.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_stat_kernel(const __grid_constant__ BwdParams p, const __nv_bfloat16 *out,
@@ -104,8 +105,8 @@ __global__ void __launch_bounds__(256) bwd_stat_kernel(const __grid_constant__ B
         for (int o = L / 2; o; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
         if (sub == 0 && slab < slabs) {
             float *s = stat + (slab * p.qtiles + r / kTile) * kStat + r % kTile;
-            s[0] = x;
-            s[kTile] = x == CUDART_INF_F ? 0.f : d;
+            s[0] = -x;
+            s[kTile] = x == CUDART_INF_F ? 0.f : -d;
         }
     }
     const FwdSet &s = p.plan.s;
@@ -133,13 +134,13 @@ struct Chunk {
     int64_t slab;
 };
 constexpr int kChunks = 4;
-constexpr int kReaders = 3 + kSoftWarps;     // warps that read a chunk: copy, 2 MMA, softmax
+template <bool KEY> constexpr int kReaders = (KEY ? 3 : 2) + kSoftWarps;   // warps that read a chunk: MMA, softmax
 template <int D> struct alignas(1024) Shared {
     uint8_t a0[Cfg<D>::UB][Cfg<D>::TILE], a1[Cfg<D>::UB][Cfg<D>::TILE];
     uint8_t b0[Cfg<D>::STAGES][Cfg<D>::TILE], b1[Cfg<D>::STAGES][Cfg<D>::TILE];
     float stat[Cfg<D>::STAGES][kStat];
     uint64_t u_full[2], u_empty[2], st_full[4], st_empty[4], tail;
-    uint64_t s_full, dp_full, s_free, p_full, ds_full, v_done, k_done, acc_full, acc_free, drain[2];
+    uint64_t s_full, dp_full, s_free, p_full, ds_full, v_done, k_done, acc_full, acc_free, drain[3];
     uint64_t ch_full[kChunks], ch_empty[kChunks];
     Chunk ch[kChunks];
     uint32_t tmem_base;
@@ -226,23 +227,6 @@ template <bool KEY> __device__ __forceinline__ bool walk_next(const BwdParams &p
     }
     return true;
 }
-// Warp 3: the CTA's chunks, a few ahead of the warps that work on them.
-template <int D, bool KEY> __device__ void chunk_role(const BwdParams &p, Shared<D> &sh, int lane) {
-    Walk w = walk_begin(p, lane);
-    for (uint32_t i = 0;; ++i) {
-        const int at = i % kChunks;
-        if (!__all_sync(0xffffffffu, wait_soon(&sh.ch_empty[at], ((i / kChunks) & 1) ^ 1, &sh.abort_flag, p.status))) return;
-        Chunk c{};
-        const bool more = walk_next<KEY>(p, w, c, lane == 0);
-        if (!more) c.nt = -1;
-        if (lane == 0) {
-            sh.ch[at] = c;
-            mbar_arrive(&sh.ch_full[at]);
-        }
-        __syncwarp();
-        if (!more) return;
-    }
-}
 // The i-th chunk, or null at the end (and after a wait that expired: `ok` false).
 template <int D>
 __device__ __forceinline__ const Chunk *chunk_at(const BwdParams &p, Shared<D> &sh, uint32_t i, bool &ok) {
@@ -254,6 +238,7 @@ template <int D> __device__ __forceinline__ void chunk_done(Shared<D> &sh, uint3
     warp_arrive(&sh.ch_empty[i % kChunks], lane);
 }
 
+// The CTA's chunks, and the copies of their tiles.
 template <int D, bool KEY>
 __device__ void copy_role(const BwdParams &p, const BwdMaps &maps, Shared<D> &sh, int lane) {
     using C = Cfg<D>;
@@ -266,11 +251,20 @@ __device__ void copy_role(const BwdParams &p, const BwdMaps &maps, Shared<D> &sh
         for (int h = 0; h < C::HALVES; ++h) tma_load_3d(dst + h * (kTile * 128), map, bar, 64 * h, row, slab);
     };
     uint32_t u = 0, g = 0, ntail = 0;
-    bool ok = true;
-    const Chunk *cp;
-    for (uint32_t i = 0; ok && (cp = chunk_at<D>(p, sh, i, ok)); ++i) {
-        const Chunk c = *cp;
-        chunk_done<D>(sh, i, lane);
+    bool ok = true, more = true;
+    Walk walk = walk_begin(p, lane);
+    for (uint32_t i = 0; ok; ++i) {
+        const int at = i % kChunks;
+        if (!(ok = wait_w(&sh.ch_empty[at], ((i / kChunks) & 1) ^ 1))) break;
+        Chunk c{};
+        more = walk_next<KEY>(p, walk, c, lane == 0);
+        if (!more) c.nt = -1;
+        if (lane == 0) {
+            sh.ch[at] = c;
+            mbar_arrive(&sh.ch_full[at]);
+        }
+        __syncwarp();
+        if (!more) break;
         if (c.nt == 0) continue;
         const int ub = u % C::UB;
         if (!(ok = wait_w(&sh.u_empty[ub], ((u / C::UB) & 1) ^ 1))) break;
@@ -390,23 +384,18 @@ __device__ void score_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int
     drain_bar(&sh.drain[0], 0);
 }
 
-// acc0 += P·B1 (KEY) and acc1 += dS·B0 of every step.
-template <int D, bool KEY>
+// acc0 += P·B1 (V) or acc1 += dS·B0 of every step.
+template <int D, bool KEY, bool V>
 __device__ void grad_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int lane) {
     using C = Cfg<D>;
+    constexpr uint32_t A_STEP = kInPlace<D, KEY> ? 32 : 16;    // columns of P and dS from w to w + 1
     volatile int *abort_flag = &sh.abort_flag;
     const bool leader = elect_one();
     auto wait_w = [&](uint64_t *b, uint32_t par) -> bool {
         return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
-    const uint64_t b0 = desc_mnmajor_sw128(sh.b0[0], kTile * 128), b1 = desc_mnmajor_sw128(sh.b1[0], kTile * 128);
-    auto product = [&](uint32_t acc, uint32_t a, uint32_t a_step, uint64_t b, bool first) __attribute__((always_inline)) {
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)        // blocks of 16 columns of the step
-            mma_ts(tmem + acc, tmem + a + a_step * (kk >> 1) + 8u * (kk & 1), b + 128 * kk, idesc_of(D, true),
-                   (first && kk == 0) ? 0u : 1u);
-    };
-    constexpr uint32_t STEP = kInPlace<D, KEY> ? 32 : 16;
+    const uint64_t b0 = desc_mnmajor_sw128(V ? sh.b1[0] : sh.b0[0], kTile * 128);
+    const uint32_t acc = tmem + (V ? kColV<D, KEY> : kColK<D, KEY>), from = tmem + (V ? col_p<D, KEY>(0) : col_ds<D, KEY>(0));
     uint32_t u = 0, g = 0;
     bool ok = true;
     const Chunk *cp;
@@ -418,29 +407,23 @@ __device__ void grad_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int 
         ++u;
         for (int t = 0; t < nt; ++t, ++g) {
             const int st = g % C::STAGES;
-            if (KEY) {
-                if (!(ok = wait_w(&sh.p_full, g & 1))) break;
-                fence_after();
-                if (leader) {
-                    product(kColV<D, KEY>, col_p<D, KEY>(0), STEP, b1 + (uint64_t)(st * (C::TILE >> 4)), t == 0);
-                    if (kInPlace<D, KEY>) commit(&sh.v_done);
-                }
-                __syncwarp();
-            }
-            if (!(ok = wait_w(&sh.ds_full, g & 1))) break;
+            if (!(ok = wait_w(V ? &sh.p_full : &sh.ds_full, g & 1))) break;
             fence_after();
             if (leader) {
-                product(kColK<D, KEY>, col_ds<D, KEY>(0), STEP, b0 + (uint64_t)(st * (C::TILE >> 4)), t == 0);
-                commit(&sh.k_done);
+                const uint64_t b = b0 + (uint64_t)(st * (C::TILE >> 4));
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)        // blocks of 16 columns of the step
+                    mma_ts(acc, from + A_STEP * (kk >> 1) + 8u * (kk & 1), b + 128 * kk, idesc_of(D, true), t > 0 || kk > 0);
+                commit(V ? &sh.v_done : &sh.k_done);
                 commit(&sh.st_empty[st]);
                 if (t + 1 == nt) commit(&sh.acc_full);
             }
             __syncwarp();
         }
     }
-    if (leader) commit(&sh.drain[1]);
+    if (leader) commit(&sh.drain[V ? 1 : 2]);
     __syncwarp();
-    drain_bar(&sh.drain[1], 0);
+    drain_bar(&sh.drain[V ? 1 : 2], 0);
 }
 
 // 32 columns of a gradient row: bf16 to dst16, or fp32 to dst32 (dst16 null).
@@ -462,7 +445,7 @@ __device__ __forceinline__ void grad32(__nv_bfloat16 *dst16, float *dst32, const
 
 // Of 16 pairs of exponentials, how many take the polynomial on the FMA pipe.
 #ifndef KPOLYB
-#define KPOLYB 4
+#define KPOLYB 0
 #endif
 constexpr int kPoly = KPOLYB;
 
@@ -483,7 +466,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
     for (uint32_t i = 0; ok && (cp = chunk_at<D>(p, sh, i, ok)); ++i) {
         const int nt = uniform(cp->nt), cols = uniform(cp->cols);
         const bool counts = row < cp->rows;
-        float lse = CUDART_INF_F, dt = 0.f;
+        float lse = -CUDART_INF_F, dt = 0.f;       // negated
         if (!KEY && counts && nt > 0) {
             const float *st = p.stat + (cp->slab * p.qtiles + cp->tile) * kStat + row;
             lse = __ldg(st);
@@ -513,8 +496,8 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 for (int e = 0; e < 4; ++e) {
                     const float4 l4 = KEY ? ls4[4 * h + e] : make_float4(lse, lse, lse, lse);
                     const int c = 16 * h + 4 * e;
-                    e2[2 * e] = __ffma2_rn(make_float2(x[c], x[c + 1]), sl2, make_float2(-l4.x, -l4.y));
-                    e2[2 * e + 1] = __ffma2_rn(make_float2(x[c + 2], x[c + 3]), sl2, make_float2(-l4.z, -l4.w));
+                    e2[2 * e] = __ffma2_rn(make_float2(x[c], x[c + 1]), sl2, make_float2(l4.x, l4.y));
+                    e2[2 * e + 1] = __ffma2_rn(make_float2(x[c + 2], x[c + 3]), sl2, make_float2(l4.z, l4.w));
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -533,7 +516,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
             }
             // the columns that P and dS take are free: the gradients' products of the step before have read them
             // (in place: before this S and this dP began)
-            if (KEY && !IN_PLACE && g > 0 && !(ok = wait_all(&sh.k_done, (g - 1) & 1))) break;
+            if (KEY && !IN_PLACE && g > 0 && !(ok = wait_all(&sh.v_done, (g - 1) & 1))) break;
             if constexpr (KEY) {
                 fence_after();
                 uint32_t pk[16];
@@ -555,9 +538,9 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 const float4 d4 = KEY ? dd4[e] : make_float4(dt, dt, dt, dt);
                 const int c = 4 * e;
                 const float2 a = __fmul2_rn(make_float2(x[c], x[c + 1]),
-                                            __fadd2_rn(make_float2(d[c], d[c + 1]), make_float2(-d4.x, -d4.y)));
+                                            __fadd2_rn(make_float2(d[c], d[c + 1]), make_float2(d4.x, d4.y)));
                 const float2 b = __fmul2_rn(make_float2(x[c + 2], x[c + 3]),
-                                            __fadd2_rn(make_float2(d[c + 2], d[c + 3]), make_float2(-d4.z, -d4.w)));
+                                            __fadd2_rn(make_float2(d[c + 2], d[c + 3]), make_float2(d4.z, d4.w)));
                 ds[2 * e] = pack_bf16x2(a.x, a.y);
                 ds[2 * e + 1] = pack_bf16x2(b.x, b.y);
             }
@@ -569,7 +552,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
                     else if (2 * e + 1 >= valid) ds[e] &= 0xffffu;
                 }
             }
-            if (!KEY && g > 0 && !(ok = wait_all(&sh.k_done, (g - 1) & 1))) break;
+            if (!IN_PLACE && g > 0 && !(ok = wait_all(&sh.k_done, (g - 1) & 1))) break;
             fence_after();
             tmem_st16w(tw + col_ds<D, KEY>(w), ds);
             tmem_wait_st();
@@ -621,15 +604,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant_
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.u_full[i], 1);
             mbar_init(&sh.u_empty[i], 1);
-            mbar_init(&sh.drain[i], 1);
         }
+        for (int i = 0; i < 3; ++i) mbar_init(&sh.drain[i], 1);
         for (int i = 0; i < Cfg<D>::STAGES; ++i) {
             mbar_init(&sh.st_full[i], 1);
-            mbar_init(&sh.st_empty[i], 2);
+            mbar_init(&sh.st_empty[i], KEY ? 3 : 2);     // the MMA warps
         }
         for (int i = 0; i < kChunks; ++i) {
             mbar_init(&sh.ch_full[i], 1);
-            mbar_init(&sh.ch_empty[i], kReaders);
+            mbar_init(&sh.ch_empty[i], kReaders<KEY>);
         }
         mbar_init(&sh.tail, 1);
         mbar_init(&sh.s_full, 1);
@@ -639,7 +622,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant_
         mbar_init(&sh.ds_full, kSoftWarps);
         mbar_init(&sh.v_done, 1);
         mbar_init(&sh.k_done, 1);
-        mbar_init(&sh.acc_full, 1);
+        mbar_init(&sh.acc_full, KEY ? 2 : 1);
         mbar_init(&sh.acc_free, kSoftWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -656,8 +639,8 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant_
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
         if (warp == 0) copy_role<D, KEY>(p, maps, sh, lane);
         else if (warp == 1) score_role<D, KEY>(p, sh, tmem, lane);
-        else if (warp == 2) grad_role<D, KEY>(p, sh, tmem, lane);
-        else chunk_role<D, KEY>(p, sh, lane);
+        else if (warp == 3) grad_role<D, KEY, false>(p, sh, tmem, lane);
+        else if (KEY) grad_role<D, KEY, true>(p, sh, tmem, lane);
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
         softmax_role<D, KEY>(p, sh, tmem, (warp - 4) >> 2, warp & 3, lane);

@@ -16,14 +16,15 @@
 //   warp 3       finds the CTA's units and hands them out
 //   warps 4-7, 8-11  softmax and epilogue of pipeline 0 and of pipeline 1
 // Many rows: the pipelines hold two tiles of 128 rows of one unit and both take
-// every key tile, so K and V are read once for 256 rows. A thread owns a row. A step
-// is half a key tile, and S has two buffers: the MMA warp issues S(0) S(1) PV(0) S(2)
-// PV(1) ..., so that the products of one step, from the arrival of its P to the next S
-// (about 1,000 clocks), run beside the softmax of the other. P(u) takes the place of
-// S(u), which S(u+2) overwrites behind P·V(u). With steps of a whole tile, P had
-// to wait for the P·V before it and every step paid that chain (2.09 us for 256 rows
-// and 128 keys at D = 64, where the exponentials alone need 1.08); two threads a row did
-// not help, the chain was the same.
+// every key tile, so K and V are read once for 256 rows. A thread owns a row.
+//   D = 64: a step is a key tile. S of the next one is formed as soon as this one's is read, and
+//   P has columns of its own; a thread keeps P in registers until the P·V before it has read
+//   those (waiting for that ahead of the exponentials put P·V's whole chain, from the arrival of P to
+//   its completion about 1,000 clocks, into every step: 2.09 us for 256 rows and 128 keys, where the
+//   exponentials alone need 1.08).
+//   D = 128: tensor memory has no columns left for that. A step is half a key tile, S has two buffers,
+//   P(u) takes the place of S(u): the MMA warp issues S(0) S(1) PV(0) S(2) PV(1) ..., so that the
+//   products of one step run beside the softmax of the other.
 // Few rows (at most 32: a decoding step's query heads, or an ensemble's members
 // together): both pipelines hold the same rows, four times over in the four 32-lane
 // quarters of tensor memory, and take alternate key tiles; warp w of a pipeline does
@@ -31,10 +32,9 @@
 // So the exponentials of a tile are spread over four warps although there are few
 // rows, and the eight partial rows are merged by their maxima and sums at the end.
 //
-// Tensor memory (512 columns): many rows: S buffer b of pipeline p 128p + 64b.., O 256 + D·p..
-// Few rows: D = 64: S0 S1 (128 each), P0 P1 (64 each), O0 O1 (64 each); S of the next tile is
-// formed while this one's softmax runs. D = 128: S0 S1, O0 O1 (128 each); P takes the first
-// 64 columns of its S, and S of the next tile follows P·V.
+// Tensor memory (512 columns): D = 64: S0 S1 (128 each), P0 P1 (64 each), O0 O1 (64 each). D = 128: S0
+// S1, O0 O1 (128 each), many rows: S in two buffers of 64, P in the first 32 columns of its buffer; few
+// rows: P in the first 64 columns of its S, and S of the next tile follows P·V.
 //
 // Keys behind a length: scores are replaced before the maximum (whatever K holds),
 // and the copy warp zeroes those rows of V in shared memory, since 0·NaN is NaN.
@@ -62,7 +62,6 @@ constexpr int kSub = 64;                    // keys of a step when there are man
 // exponentials (a step of 256 rows and 128 keys: none 1.86 us, 4 of 16 1.69, 6 of 16 1.75), D = 128
 // by the chain of its products (none 2.33 us, 4 of 16 2.44).
 template <int D> constexpr int kPoly = D == 64 ? 4 : 0;
-constexpr int GRP = 8;                      // pairs in a phase
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -296,22 +295,22 @@ __device__ void copy_role(const FwdParams &p, const Maps &maps, Shared<D> &sh, i
 }
 
 __device__ __forceinline__ uint32_t col_s(int pl) { return 128u * pl; }
-template <int D, bool FEW> __device__ __forceinline__ uint32_t col_o(int pl) {
-    return FEW && D == 64 ? 384u + 64u * pl : 256u + (uint32_t)D * pl;
-}
-// few rows
+template <int D> __device__ __forceinline__ uint32_t col_o(int pl) { return D == 64 ? 384u + 64u * pl : 256u + 128u * pl; }
 template <int D> __device__ __forceinline__ uint32_t col_p(int pl) { return D == 64 ? 256u + 64u * pl : 128u * pl; }
+// Steps of a whole key tile (else of half a tile, with two buffers of S).
+template <int D, bool FEW> constexpr bool kWhole = FEW || D == 64;
 
-// Steps of 64 keys of a chunk (many rows).
+// Steps of 64 keys of a chunk.
 __device__ __forceinline__ int sub_steps(int nt, int rel) { return (min(rel, nt * kTile) + kSub - 1) / kSub; }
 
 template <int D, bool FEW>
 __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int pl, int lane) {
     using C = Cfg<D>;
-    constexpr int KEYS = FEW ? kTile : kSub;           // keys of a step
+    constexpr bool WHOLE = kWhole<D, FEW>;
+    constexpr int KEYS = WHOLE ? kTile : kSub;         // keys of a step
     volatile int *abort_flag = &sh.abort_flag;
     const bool leader = elect_one();    // issues; the whole warp runs the loop
-    const uint32_t tS = tmem + col_s(pl), tP = FEW ? tmem + col_p<D>(pl) : tS, tO = tmem + col_o<D, FEW>(pl);
+    const uint32_t tS = tmem + col_s(pl), tP = tmem + col_p<D>(pl), tO = tmem + col_o<D>(pl);
     const uint64_t dq = desc_kmajor_sw128(sh.q[pl]);
     const uint64_t dk0 = desc_kmajor_sw128(sh.kv[0]), dv0 = desc_mnmajor_sw128(sh.kv[0], kTile * 128);
     uint32_t pos = 0, g = 0, nq = 0;       // ring position, this pipeline's steps and units
@@ -333,7 +332,7 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t off = (kk / 4) * ((kTile * 128) >> 4) + 2 * (kk % 4);
-                mma_bf16(tS + (FEW ? 0u : 64u * b), dq + off, dk + off, idesc_of(KEYS, false), kk > 0);
+                mma_bf16(tS + (WHOLE ? 0u : 64u * b), dq + off, dk + off, idesc_of(KEYS, false), kk > 0);
             }
             commit(&sh.s_full[pl][b]);
             if (done) release(st, alone);
@@ -350,7 +349,7 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
             const uint64_t dv = dv0 + (uint64_t)(st * (C::TILE >> 4) + from * 8);
 #pragma unroll
             for (int kk = 0; kk < KEYS / 16; ++kk)
-                mma_ts(tO, tP + (FEW ? 0u : 64u * b) + 8u * kk, dv + 128 * kk, idesc_of(D, true), (first && kk == 0) ? 0u : 1u);
+                mma_ts(tO, tP + (WHOLE ? 0u : 64u * b) + 8u * kk, dv + 128 * kk, idesc_of(D, true), (first && kk == 0) ? 0u : 1u);
             commit(&sh.o_done[pl][b]);
             if (done) release(st, alone);
         }
@@ -367,26 +366,28 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
         if (nt > 0 && (FEW || pl == 0 || !alone)) {
             if (!(ok = wait_w(&sh.q_full[pl], nq & 1))) break;
             ++nq;
-            if constexpr (FEW) {                       // every other tile
-                if (pl >= nt) {                        // one tile: this pipeline's Q stays unused
+            if constexpr (WHOLE) {
+                constexpr int by = FEW ? 2 : 1;        // few rows: every other tile
+                const int first = FEW ? pl : 0;
+                if (first >= nt) {                     // one tile: this pipeline's Q stays unused
                     if (leader) mbar_arrive(&sh.q_empty[pl]);
                     __syncwarp();
                 } else {
                     constexpr bool ahead = D == 64 && C::STAGES >= 6;
-                    if (!(ok = there(pos + 2 * pl))) break;
-                    issue_s(g, pos + 2 * pl, 0, true, true, pl + 2 >= nt);
-                    for (int t = pl; t < nt && ok; t += 2) {
-                        const bool more = t + 2 < nt;
-                        const uint32_t kn = pos + 2 * (t + 2), v = pos + 2 * t + 1;
+                    if (!(ok = there(pos + 2 * first))) break;
+                    issue_s(g, pos + 2 * first, 0, true, alone, first + by >= nt);
+                    for (int t = first; t < nt && ok; t += by) {
+                        const bool more = t + by < nt;
+                        const uint32_t kn = pos + 2 * (t + by), v = pos + 2 * t + 1;
                         if (ahead) {                   // P has columns of its own: S as soon as the last one is read
                             if (more) {
                                 if (!(ok = there(kn) && wait_w(&sh.s_free[pl], g & 1))) break;
-                                issue_s(g + 1, kn, 0, true, true, t + 4 >= nt);
+                                issue_s(g + 1, kn, 0, true, alone, t + 2 * by >= nt);
                             }
-                            ok = there(v) && issue_pv(v, 0, true, true, t == pl);
+                            ok = there(v) && issue_pv(v, 0, true, alone, t == first);
                         } else {
-                            ok = there(v) && issue_pv(v, 0, true, true, t == pl) && (!more || there(kn));
-                            if (ok && more) issue_s(g, kn, 0, true, true, t + 4 >= nt);
+                            ok = there(v) && issue_pv(v, 0, true, alone, t == first) && (!more || there(kn));
+                            if (ok && more) issue_s(g, kn, 0, true, alone, t + 2 * by >= nt);
                         }
                     }
                 }
@@ -426,26 +427,36 @@ __device__ __forceinline__ float sum4(const float2 *a) {
     const float2 t = __fadd2_rn(__fadd2_rn(a[0], a[1]), __fadd2_rn(a[2], a[3]));
     return t.x + t.y;
 }
-// 32 scores of a row to bf16 pairs of 2^(s·sl2 - m), and their sums onto acc. GRP pairs at a time, in
-// three phases (exponents, exponentials, then packing and four chains of sums), so that in-order issue
-// does not wait on one result while independent work could be queued. POLY of 16 pairs take the
-// polynomial on the FMA pipe instead of the exp unit.
-template <int POLY>
-__device__ __forceinline__ void numerators32(const float *s, float sl2, float neg_m, uint32_t *pk, float2 *acc) {
+// PAIRS pairs of a row's scores to bf16 pairs of 2^(s·sl2 - m), and their sums onto acc (four chains).
+// In rotation: exponentials of pair c, the exponent of pair c + AHEAD, packing and sum of pair
+// c - AHEAD, so that the other work goes out between the exponentials, of which the exp unit takes
+// one instruction in eight clocks (issued in a row they fill its queue, and a warp that waits there
+// issues nothing else). POLY of 16 pairs take the polynomial on the FMA pipe instead.
+template <int POLY, int PAIRS>
+__device__ __forceinline__ void numerators(const float *s, float sl2, float neg_m, uint32_t *pk, float2 *acc) {
+    constexpr int AHEAD = 4;
     const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(neg_m, neg_m);
+    float2 x[2 * AHEAD + 1];
+    auto at = [](int c) { return c % (2 * AHEAD + 1); };
 #pragma unroll
-    for (int h = 0; h < 16; h += GRP) {
-        float2 x[GRP];
+    for (int c = 0; c < AHEAD && c < PAIRS; ++c) x[at(c)] = __ffma2_rn(make_float2(s[2 * c], s[2 * c + 1]), sc2, nm2);
 #pragma unroll
-        for (int c = 0; c < GRP; ++c) x[c] = __ffma2_rn(make_float2(s[2 * (h + c)], s[2 * (h + c) + 1]), sc2, nm2);
-#pragma unroll
-        for (int c = 0; c < GRP; ++c)
-            x[c] = (h + c) * POLY % 16 < POLY ? exp2_fma2(x[c]) : make_float2(ex2(x[c].x), ex2(x[c].y));
-#pragma unroll
-        for (int c = 0; c < GRP; ++c) {
-            pk[h + c] = pack_bf16x2(x[c].x, x[c].y);
-            acc[c & 3] = __fadd2_rn(acc[c & 3], x[c]);
+    for (int c = 0; c < PAIRS + AHEAD; ++c) {
+        if (c < PAIRS) {
+            float2 &y = x[at(c)];
+            if (c * POLY % 16 < POLY) {
+                y = exp2_fma2(y);
+            } else {
+                asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(y.x));
+                asm volatile("ex2.approx.ftz.f32 %0, %0;" : "+f"(y.y));
+            }
         }
+        if (c >= AHEAD) {
+            const float2 y = x[at(c - AHEAD)];
+            asm volatile("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(pk[c - AHEAD]) : "f"(y.y), "f"(y.x));
+            acc[c & 3] = __fadd2_rn(acc[c & 3], y);
+        }
+        if (c + AHEAD < PAIRS) x[at(c + AHEAD)] = __ffma2_rn(make_float2(s[2 * (c + AHEAD)], s[2 * (c + AHEAD) + 1]), sc2, nm2);
     }
 }
 
@@ -503,7 +514,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
     const unsigned FULL = 0xffffffffu;
     volatile int *abort_flag = &sh.abort_flag;
     const uint32_t wl = (uint32_t)(32 * wq) << 16;
-    const uint32_t tS = tmem + col_s(pl) + wl, tO = tmem + col_o<D, FEW>(pl) + wl;
+    const uint32_t tS = tmem + col_s(pl) + wl, tO = tmem + col_o<D>(pl) + wl, tP = tmem + col_p<D>(pl) + wl;
     const float sl2 = p.scale_log2;
     uint32_t g = 0, nmerge = 0;
     bool ok = true;
@@ -545,33 +556,62 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 chunk_done<D>(sh, i, lane);
                 continue;
             }
-            const int n = nt > 0 ? sub_steps(nt, rel) : 0;
-            for (int u = 0; u < n; ++u, ++g) {
-                const uint32_t tSu = tS + 64u * (g & 1);
-                if (!(ok = wait_all(&sh.s_full[pl][g & 1], (g >> 1) & 1))) break;
-                fence_after();
-                float x[kSub];
-                tmem_ld32(tSu, x);
-                tmem_ld32(tSu + 32, x + 32);
-                tmem_wait_ld_of(x);
-                const int valid = rel - u * kSub;      // keys behind the length count as -inf
-                if (valid < kSub) {
+            const int n = nt <= 0 ? 0 : (D == 64 ? nt : sub_steps(nt, rel));
+            if constexpr (D == 64) {
+                for (int t = 0; t < n; ++t, ++g) {
+                    if (!(ok = wait_all(&sh.s_full[pl][g & 1], (g >> 1) & 1))) break;
+                    fence_after();
+                    float x[kTile];
 #pragma unroll
-                    for (int e = 0; e < kSub; ++e) x[e] = e < valid ? x[e] : -CUDART_INF_F;
-                }
-                if (!(ok = new_max(sl2 * fmaxf(max32(x), max32(x + 32)), m, l, u > 0))) break;
-                const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
-                float2 acc[4] = {};
+                    for (int cc = 0; cc < kTile; cc += 32) tmem_ld32(tS + cc, x + cc);
+                    tmem_wait_ld_of(x);
+                    fence_before();
+                    warp_arrive(&sh.s_free[pl], lane);
+                    const int valid = rel - t * kTile;     // keys behind the length count as -inf
+                    if (valid < kTile) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t pk[16];
-                    numerators32<kPoly<D>>(x + 32 * h, sl2, neg_m, pk, acc);
-                    tmem_st16w(tSu + 16 * h, pk);
+                        for (int e = 0; e < kTile; ++e) x[e] = e < valid ? x[e] : -CUDART_INF_F;
+                    }
+                    const float mx = sl2 * fmaxf(fmaxf(max32(x), max32(x + 32)), fmaxf(max32(x + 64), max32(x + 96)));
+                    if (!(ok = new_max(mx, m, l, t > 0))) break;
+                    const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+                    float2 acc[4] = {};
+                    uint32_t pk[kTile / 2];
+                    numerators<kPoly<D>, kTile / 2>(x, sl2, neg_m, pk, acc);
+                    l += sum4(acc);
+                    if (t > 0 && !(ok = wait_o())) break;  // P's columns are read
+                    fence_after();
+                    tmem_st32(tP, reinterpret_cast<const float *>(pk));
+                    tmem_st32(tP + 32, reinterpret_cast<const float *>(pk + 32));
+                    tmem_wait_st();
+                    fence_before();
+                    warp_arrive(&sh.p_full[pl][g & 1], lane);
                 }
-                l += sum4(acc);
-                tmem_wait_st();
-                fence_before();
-                warp_arrive(&sh.p_full[pl][g & 1], lane);
+            } else {
+                for (int u = 0; u < n; ++u, ++g) {
+                    const uint32_t tSu = tS + 64u * (g & 1);
+                    if (!(ok = wait_all(&sh.s_full[pl][g & 1], (g >> 1) & 1))) break;
+                    fence_after();
+                    float x[kSub];
+                    tmem_ld32(tSu, x);
+                    tmem_ld32(tSu + 32, x + 32);
+                    tmem_wait_ld_of(x);
+                    const int valid = rel - u * kSub;      // keys behind the length count as -inf
+                    if (valid < kSub) {
+#pragma unroll
+                        for (int e = 0; e < kSub; ++e) x[e] = e < valid ? x[e] : -CUDART_INF_F;
+                    }
+                    if (!(ok = new_max(sl2 * fmaxf(max32(x), max32(x + 32)), m, l, u > 0))) break;
+                    const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
+                    float2 acc[4] = {};
+                    uint32_t pk[kSub / 2];
+                    numerators<kPoly<D>, kSub / 2>(x, sl2, neg_m, pk, acc);
+                    tmem_st32(tSu, reinterpret_cast<const float *>(pk));
+                    l += sum4(acc);
+                    tmem_wait_st();
+                    fence_before();
+                    warp_arrive(&sh.p_full[pl][g & 1], lane);
+                }
             }
             if (!ok || (n > 0 && !(ok = wait_o()))) break;
             fence_after();
@@ -594,7 +634,6 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
             fence_before();
             chunk_done<D>(sh, i, lane);
         } else {
-        const uint32_t tP = tmem + col_p<D>(pl) + wl;
         // few rows: this warp's keys are 32·wq .. +31 of each of its pipeline's tiles
         const int nrows = (int)(p.plan.s.members * p.plan.rows);
         bool any = false;
@@ -615,7 +654,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
             if (!(ok = new_max(mx, m, l, any))) break;
             float2 acc[4] = {};
             uint32_t pk[16], zero[16];
-            numerators32<0>(x, sl2, m == -CUDART_INF_F ? 0.f : -m, pk, acc);
+            numerators<0, 16>(x, sl2, m == -CUDART_INF_F ? 0.f : -m, pk, acc);
             if (D == 64 && any && !(ok = wait_o())) break;   // P is read
             any = true;
             fence_after();

@@ -61,6 +61,10 @@ __device__ __forceinline__ void tmem_wait_ld_of(float (&x)[64]) {
         :
         : "memory");
 }
+__device__ __forceinline__ void tmem_wait_ld_of(float (&x)[128]) {
+    tmem_wait_ld_of(*reinterpret_cast<float (*)[64]>(&x[0]));
+    tmem_wait_ld_of(*reinterpret_cast<float (*)[64]>(&x[64]));
+}
 // Bounded wait (2 s, as wait_bar) that does not read the global timer, which costs more than most waits
 // last, before it has been suspended a few times.
 __device__ __forceinline__ bool wait_soon(uint64_t *b, uint32_t parity, volatile int *abort_flag, uint32_t *status) {
@@ -100,7 +104,8 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-125.f));
     asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-125.f));
     const float2 t = __fadd2_rn(x, make_float2(0x1.8p23f, 0x1.8p23f));           // low bits: n
-    const float2 f = __fadd2_rn(x, __fadd2_rn(make_float2(0x1.8p23f, 0x1.8p23f), make_float2(-t.x, -t.y)));
+    const float2 n = __fadd2_rn(t, make_float2(-0x1.8p23f, -0x1.8p23f));
+    const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);                 // x - n, exact
     float2 p = __ffma2_rn(f, make_float2(0x1.c3f76p-5f, 0x1.c3f76p-5f), make_float2(0x1.f0de1ap-3f, 0x1.f0de1ap-3f));
     p = __ffma2_rn(p, f, make_float2(0x1.62f31ap-1f, 0x1.62f31ap-1f));
     p = __ffma2_rn(p, f, make_float2(0x1.fff692p-1f, 0x1.fff692p-1f));
