@@ -196,7 +196,7 @@ template <bool KEY> __device__ __forceinline__ bool walk_next(const BwdParams &p
     } else {
         const int64_t per = KEY ? hk_n * ((s.n + kTile - 1) / kTile) : s.upz;
         if (w.left >= s.sets * per) return false;
-        z = w.left / per;
+        z = quotient(w.left, per);
         uu = w.left - z * per;
         c.t0 = 0;
         n = KEY ? s.fixed : 0x7fffffff;
@@ -204,7 +204,7 @@ template <bool KEY> __device__ __forceinline__ bool walk_next(const BwdParams &p
     }
     const int len = set_len(s.len, z, s.n, lead ? p.status : nullptr);
     const int64_t tiles = KEY ? (p.plan.stream ? set_steps(s, z) : (s.n + kTile - 1) / kTile) : s.tiles;
-    const int64_t hk = uu / tiles;
+    const int64_t hk = quotient(uu, tiles);
     c.tile = (int)(uu - hk * tiles);
     c.slab = z * hk_n + hk;
     if (p.plan.stream) {
@@ -426,23 +426,6 @@ __device__ void grad_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int 
     drain_bar(&sh.drain[V ? 1 : 2], 0);
 }
 
-// 32 columns of a gradient row: bf16 to dst16, or fp32 to dst32 (dst16 null).
-__device__ __forceinline__ void grad32(__nv_bfloat16 *dst16, float *dst32, const float *x, float f) {
-    if (dst16) {
-        uint4 *d4 = reinterpret_cast<uint4 *>(dst16);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            d4[c] = make_uint4(pack_bf16x2(x[8 * c] * f, x[8 * c + 1] * f), pack_bf16x2(x[8 * c + 2] * f, x[8 * c + 3] * f),
-                               pack_bf16x2(x[8 * c + 4] * f, x[8 * c + 5] * f), pack_bf16x2(x[8 * c + 6] * f, x[8 * c + 7] * f));
-    } else {
-        float4 *d4 = reinterpret_cast<float4 *>(dst32);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            d4[c] = make_float4(x[4 * c] * f, x[4 * c + 1] * f, x[4 * c + 2] * f, x[4 * c + 3] * f);
-    }
-}
-
-
 // Of 16 pairs of exponentials, how many take the polynomial on the FMA pipe.
 #ifndef KPOLYB
 #define KPOLYB 0
@@ -571,25 +554,25 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
         const uint32_t col = grad == 0 ? kColV<D, KEY> : kColK<D, KEY>;
         const int64_t at = cp->slab * (KEY ? p.plan.s.n : p.plan.rows) + (int64_t)cp->tile * kTile + row;
         const int slot = cp->slot;
-        __nv_bfloat16 *d16 = slot >= 0 ? nullptr : (!KEY ? p.dq : grad == 0 ? p.dv : p.dk) + at * D;
+        __nv_bfloat16 *d16 = (!KEY ? p.dq : grad == 0 ? p.dv : p.dk) + at * D;
         float *d32 = p.part + ((2 * (int64_t)blockIdx.x + max(slot, 0)) * kTile + row) * (KEY ? 2 * D : D) + (KEY ? grad * D : 0);
-        if (!KEY || nt > 0) {
-#pragma unroll 1
-            for (int cc = part * wide; cc < min(D, (part + 1) * wide); cc += 32) {
-                float y[32];
-                if (nt > 0) {
-                    tmem_ld32(tw + col + cc, y);
-                    tmem_wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) y[e] = 0.f;
-                }
-                if (counts) grad32(d16 ? d16 + cc : nullptr, d32 + cc, y, grad == 0 ? 1.f : p.scale);
-                __syncwarp();
-            }
+        const int c0 = part * wide;
+        if (nt > 0 && c0 < D) {
+            // staged in the unit's own tiles, which no product reads any more
+            const int ub = (u + C::UB - 1) % C::UB;
+            uint8_t *stage = (4 * w + wq < 8 ? sh.a0[ub] : sh.a1[ub]) + 2048 * ((4 * w + wq) & 7);
+            write_rows(stage, tw + col + c0, wide, grad == 0 ? 1.f : p.scale, false, slot < 0,
+                       slot < 0 ? static_cast<void *>(d16 + c0) : d32 + c0, counts, lane);
+        } else if (!KEY && c0 < D && counts) {         // no keys: zeros (and the unit has no tiles here)
+            for (int e = 0; e < 4; ++e) reinterpret_cast<uint4 *>(d16 + c0)[e] = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_before();
-        if (nt > 0) warp_arrive(&sh.acc_free, lane);
+        if (nt > 0) {
+            // the staged rows are read, and the copies may overwrite them (another proxy)
+            fence_proxy_async();
+            warp_arrive(&sh.u_empty[(u + C::UB - 1) % C::UB], lane);
+            warp_arrive(&sh.acc_free, lane);
+        }
         chunk_done<D>(sh, i, lane);
     }
 }
@@ -603,7 +586,7 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant_
         sh.abort_flag = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.u_full[i], 1);
-            mbar_init(&sh.u_empty[i], 1);
+            mbar_init(&sh.u_empty[i], 1 + kSoftWarps);     // the scores' products, and the epilogue
         }
         for (int i = 0; i < 3; ++i) mbar_init(&sh.drain[i], 1);
         for (int i = 0; i < Cfg<D>::STAGES; ++i) {
@@ -625,6 +608,12 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant_
         mbar_init(&sh.acc_full, KEY ? 2 : 1);
         mbar_init(&sh.acc_free, kSoftWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&maps.a0);
+        prefetch_map(&maps.a1);
+        prefetch_map(&maps.b0);
+        prefetch_map(&maps.b1);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem_base))

@@ -52,16 +52,22 @@ namespace {
 
 using namespace tc;
 
-constexpr int NTHREADS = 384;
-constexpr int kCtrlRegs = 72, kSoftRegs = 216;
-constexpr int kRegsNeeded = 128 * kCtrlRegs + 256 * kSoftRegs;
-static_assert(kRegsNeeded <= 65536, "register split");
-constexpr int kReaders = 11;                // warps that read a chunk: copy, 2 MMA, 8 softmax
+// Threads of a row: two where tensor memory has room for P beside S (half of a tile's keys each).
+template <int D, bool FEW> struct Threads {
+    static constexpr int SPLIT = !FEW && D == 64 ? 2 : 1;
+    static constexpr int SOFT_WARPS = 4 * SPLIT;       // a pipeline
+    static constexpr int ALL = 128 + 64 * SOFT_WARPS;
+    // register split: the control warpgroup drops to CTRL registers a thread, the softmax warps rise to SOFT
+    static constexpr int CTRL = SPLIT == 2 ? 56 : 72, SOFT = SPLIT == 2 ? 104 : 216;
+    static constexpr int REGS = 128 * CTRL + 64 * SOFT_WARPS * SOFT;
+    static constexpr int READERS = 3 + 2 * SOFT_WARPS; // warps that read a chunk: copy, 2 MMA, softmax
+    static_assert(REGS <= 65536 / ALL / 8 * 8 * ALL, "register split");
+};
 constexpr int kSub = 64;                    // keys of a step when there are many rows
 // Of 16 pairs of exponentials, how many take the polynomial on the FMA pipe. D = 64 is bound by the
 // exponentials (a step of 256 rows and 128 keys: none 1.86 us, 4 of 16 1.69, 6 of 16 1.75), D = 128
 // by the chain of its products (none 2.33 us, 4 of 16 2.44).
-template <int D> constexpr int kPoly = D == 64 ? 4 : 0;
+template <int D> constexpr int kPoly = D == 64 ? 2 : 0;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -93,9 +99,10 @@ template <int D> struct alignas(1024) Shared {
     uint8_t kv[Cfg<D>::STAGES][Cfg<D>::TILE];
     float merge[8][Cfg<D>::MROWS][Cfg<D>::MSTRIDE];
     float ml[2][8][32];                                // few rows: (m, l) of each partial row
+    float ls[2][2][2][kTile];                          // two threads a row: [chunk % 2][pipeline][half] sums
     uint64_t q_full[2], q_empty[2], kv_full[Cfg<D>::STAGES], kv_empty[Cfg<D>::STAGES], tail;
     uint64_t s_full[2][2], p_full[2][2], o_done[2][2];  // [pipeline][step % 2]
-    uint64_t s_free[2], merge_bar, drain[2];
+    uint64_t s_free[2], l_bar[2], merge_bar, drain[2];
     uint64_t ch_full[kChunks], ch_empty[kChunks];
     Chunk ch[kChunks];
     uint32_t tmem_base;
@@ -153,7 +160,7 @@ __device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c,
             }
         }
         c.z = w.z;
-        c.hk = w.uu / s.pairs;
+        c.hk = quotient(w.uu, s.pairs);
         c.pair = w.uu - c.hk * s.pairs;
         c.t0 = w.t;
         steps = (int)min((int64_t)(w.steps - w.t), w.left);
@@ -170,9 +177,9 @@ __device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c,
         int64_t u = w.left;
         if (u >= s.sets * s.upz) return false;
         if (lead && p.spans) p.spans[u] = make_int2(0, 0);
-        c.z = u / s.upz;
+        c.z = quotient(u, s.upz);
         u -= c.z * s.upz;
-        c.hk = u / s.pairs;
+        c.hk = quotient(u, s.pairs);
         c.pair = u - c.hk * s.pairs;
         c.t0 = 0;
         c.slot = -1;
@@ -460,28 +467,12 @@ __device__ __forceinline__ void numerators(const float *s, float sl2, float neg_
     }
 }
 
-// 32 columns of a finished row: bf16 to out or fp32 to a workspace row (dst16 null), times f.
-__device__ __forceinline__ void store32(__nv_bfloat16 *dst16, float *dst32, const float *x, float f) {
-    if (dst16) {
-        uint4 *d4 = reinterpret_cast<uint4 *>(dst16);
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            d4[c] = make_uint4(pack_bf16x2(x[8 * c] * f, x[8 * c + 1] * f), pack_bf16x2(x[8 * c + 2] * f, x[8 * c + 3] * f),
-                               pack_bf16x2(x[8 * c + 4] * f, x[8 * c + 5] * f), pack_bf16x2(x[8 * c + 6] * f, x[8 * c + 7] * f));
-    } else {
-        float4 *d4 = reinterpret_cast<float4 *>(dst32);
-#pragma unroll
-        for (int c = 0; c < 8; ++c)
-            d4[c] = make_float4(x[4 * c] * f, x[4 * c + 1] * f, x[4 * c + 2] * f, x[4 * c + 3] * f);
-    }
-}
-
 // Where row i (of the unit's 256) of a chunk goes: out and lse, a part, or a whole row of a set.
 struct RowOut {
     __nv_bfloat16 *o16;
     float *o32, *lse;
     float lse_unit;         // lse is kept in log2 units in the workspace, given out in natural ones
-    bool valid;
+    bool valid, bf16;       // bf16: o16, for all rows of the chunk
 };
 template <int D>
 __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, int64_t tile, int i_tile, int i_unit) {
@@ -491,6 +482,7 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
     r.o16 = nullptr;
     r.o32 = r.lse = nullptr;
     r.lse_unit = 1.f;
+    r.bf16 = c.slot < 0 && !p.whole_o;
     if (!r.valid) return r;
     if (c.slot >= 0) {
         const int64_t at = (2 * (int64_t)blockIdx.x + c.slot) * (2 * kTile) + i_unit;
@@ -509,14 +501,16 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
 }
 
 template <int D, bool FEW>
-__device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int pl, int wq, int lane) {
+__device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int pl, int hh, int wq, int lane) {
     using C = Cfg<D>;
+    constexpr int SPLIT = Threads<D, FEW>::SPLIT;      // threads of a row; hh: which of them this is
+    constexpr int WIDE = kTile / SPLIT, COLS = D / SPLIT;   // this thread's keys of a tile, columns of O
     const unsigned FULL = 0xffffffffu;
     volatile int *abort_flag = &sh.abort_flag;
     const uint32_t wl = (uint32_t)(32 * wq) << 16;
     const uint32_t tS = tmem + col_s(pl) + wl, tO = tmem + col_o<D>(pl) + wl, tP = tmem + col_p<D>(pl) + wl;
     const float sl2 = p.scale_log2;
-    uint32_t g = 0, nmerge = 0;
+    uint32_t g = 0, nmerge = 0, nl = 0;
     bool ok = true;
     auto wait_all = [&](uint64_t *b, uint32_t par) -> bool {
         return __all_sync(FULL, wait_soon(b, par, abort_flag, p.status));
@@ -533,13 +527,13 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
             const float alpha = need ? ex2(m - mx) : 1.f;
             fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < D; cc += 32) {
-                float o[32];
-                tmem_ld32(tO + cc, o);
+            for (int cc = COLS * hh; cc < COLS * (hh + 1); cc += 16) {
+                uint32_t o[16];
+                tmem_ld16w(tO + cc, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= alpha;
-                tmem_st32(tO + cc, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tmem_st16w(tO + cc, o);
             }
             tmem_wait_st();
             l *= alpha;
@@ -558,31 +552,43 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
             }
             const int n = nt <= 0 ? 0 : (D == 64 ? nt : sub_steps(nt, rel));
             if constexpr (D == 64) {
-                for (int t = 0; t < n; ++t, ++g) {
-                    if (!(ok = wait_all(&sh.s_full[pl][g & 1], (g >> 1) & 1))) break;
+                // one wait a step: for the next S, which its thread issued behind the P·V that has to be done with
+                // P's columns before this step's P goes there
+                ok = n == 0 || wait_all(&sh.s_full[pl][g & 1], (g >> 1) & 1);
+                for (int t = 0; t < n && ok; ++t, ++g) {
                     fence_after();
-                    float x[kTile];
+                    // both threads of a row need the maximum of the whole row: reading the other half costs
+                    // less than an exchange. Keys behind the length count as -inf.
+                    float x[WIDE], mx = -CUDART_INF_F;
+                    const int valid = rel - t * kTile;
 #pragma unroll
-                    for (int cc = 0; cc < kTile; cc += 32) tmem_ld32(tS + cc, x + cc);
-                    tmem_wait_ld_of(x);
+                    for (int h = SPLIT - 1; h >= 0; --h) {
+                        const int half = hh ^ h;       // its own half last
+#pragma unroll
+                        for (int cc = 0; cc < WIDE; cc += 32) tmem_ld32(tS + WIDE * half + cc, x + cc);
+                        tmem_wait_ld_of(x);
+                        if (valid < kTile) {
+#pragma unroll
+                            for (int e = 0; e < WIDE; ++e) x[e] = WIDE * half + e < valid ? x[e] : -CUDART_INF_F;
+                        }
+#pragma unroll
+                        for (int cc = 0; cc < WIDE; cc += 32) mx = fmaxf(mx, max32(x + cc));
+                    }
                     fence_before();
                     warp_arrive(&sh.s_free[pl], lane);
-                    const int valid = rel - t * kTile;     // keys behind the length count as -inf
-                    if (valid < kTile) {
-#pragma unroll
-                        for (int e = 0; e < kTile; ++e) x[e] = e < valid ? x[e] : -CUDART_INF_F;
-                    }
-                    const float mx = sl2 * fmaxf(fmaxf(max32(x), max32(x + 32)), fmaxf(max32(x + 64), max32(x + 96)));
-                    if (!(ok = new_max(mx, m, l, t > 0))) break;
+                    if (!(ok = new_max(sl2 * mx, m, l, t > 0))) break;
                     const float neg_m = m == -CUDART_INF_F ? 0.f : -m;
                     float2 acc[4] = {};
-                    uint32_t pk[kTile / 2];
-                    numerators<kPoly<D>, kTile / 2>(x, sl2, neg_m, pk, acc);
+                    uint32_t pk[WIDE / 2];
+                    numerators<kPoly<D>, WIDE / 2>(x, sl2, neg_m, pk, acc);
                     l += sum4(acc);
-                    if (t > 0 && !(ok = wait_o())) break;  // P's columns are read
+                    if (t + 1 < n) ok = wait_all(&sh.s_full[pl][(g + 1) & 1], ((g + 1) >> 1) & 1);
+                    else if (t > 0) ok = wait_o();
+                    if (!ok) break;
                     fence_after();
-                    tmem_st32(tP, reinterpret_cast<const float *>(pk));
-                    tmem_st32(tP + 32, reinterpret_cast<const float *>(pk + 32));
+#pragma unroll
+                    for (int cc = 0; cc < WIDE / 2; cc += 32)
+                        tmem_st32(tP + WIDE / 2 * hh + cc, reinterpret_cast<const float *>(pk + cc));
                     tmem_wait_st();
                     fence_before();
                     warp_arrive(&sh.p_full[pl][g & 1], lane);
@@ -615,22 +621,20 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
             }
             if (!ok || (n > 0 && !(ok = wait_o()))) break;
             fence_after();
+            if constexpr (SPLIT == 2) {                    // the row's sum is both threads'
+                float *ls = &sh.ls[nl & 1][pl][0][32 * wq + lane];
+                ls[kTile * hh] = l;
+                warp_arrive(&sh.l_bar[pl], lane);
+                if (!(ok = wait_all(&sh.l_bar[pl], nl & 1))) break;
+                ++nl;
+                l = ls[0] + ls[kTile];
+            }
             const RowOut r = row_out<D>(p, *cp, 2 * cp->pair + pl, 32 * wq + lane, kTile * pl + 32 * wq + lane);
             const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll 1
-            for (int cc = 0; cc < D; cc += 32) {
-                float o[32];
-                if (n > 0) {
-                    tmem_ld32(tO + cc, o);
-                    tmem_wait_ld();
-                }
-                if (n == 0 || l == 0.f) {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                }
-                if (r.valid) store32(r.o16 ? r.o16 + cc : nullptr, r.o32 + cc, o, inv);
-            }
-            if (r.valid && r.lse) *r.lse = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * r.lse_unit;
+            uint8_t *stage = reinterpret_cast<uint8_t *>(sh.merge) + 2048 * (4 * (SPLIT * pl + hh) + wq);
+            void *dst = r.bf16 ? static_cast<void *>(r.o16 + COLS * hh) : r.o32 + COLS * hh;
+            write_rows(stage, tO + COLS * hh, COLS, inv, n == 0 || l == 0.f, r.bf16, dst, r.valid, lane);
+            if (hh == 0 && r.valid && r.lse) *r.lse = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * r.lse_unit;
             fence_before();
             chunk_done<D>(sh, i, lane);
         } else {
@@ -729,6 +733,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                     }
                 }
             }
+            if (r0 + C::MROWS >= nrows) break;   // (the next chunk's first barrier comes before its first write)
             warp_arrive(&sh.merge_bar, lane);    // the buffer is free again
             if (!(ok = wait_all(&sh.merge_bar, nmerge++ & 1))) break;
         }
@@ -744,8 +749,9 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
 }
 
 template <int D, bool FEW>
-__global__ void __launch_bounds__(NTHREADS, 1) dense_fwd_kernel(const __grid_constant__ Maps maps,
+__global__ void __launch_bounds__((Threads<D, FEW>::ALL), 1) dense_fwd_kernel(const __grid_constant__ Maps maps,
                                                                 const __grid_constant__ FwdParams p) {
+    using T = Threads<D, FEW>;
     extern __shared__ uint8_t smem_raw[];
     Shared<D> &sh = *reinterpret_cast<Shared<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -754,10 +760,11 @@ __global__ void __launch_bounds__(NTHREADS, 1) dense_fwd_kernel(const __grid_con
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_empty[i], 1);
-            mbar_init(&sh.s_free[i], 4);
+            mbar_init(&sh.s_free[i], T::SOFT_WARPS);
+            mbar_init(&sh.l_bar[i], T::SOFT_WARPS);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(&sh.s_full[i][b], 1);
-                mbar_init(&sh.p_full[i][b], 4);
+                mbar_init(&sh.p_full[i][b], T::SOFT_WARPS);
                 mbar_init(&sh.o_done[i][b], 1);
             }
             mbar_init(&sh.drain[i], 1);
@@ -768,11 +775,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) dense_fwd_kernel(const __grid_con
         }
         for (int i = 0; i < kChunks; ++i) {
             mbar_init(&sh.ch_full[i], 1);
-            mbar_init(&sh.ch_empty[i], kReaders);
+            mbar_init(&sh.ch_empty[i], T::READERS);
         }
         mbar_init(&sh.tail, 1);
         mbar_init(&sh.merge_bar, 8);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_map(&maps.q);
+        prefetch_map(&maps.k);
+        prefetch_map(&maps.v);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem_base))
@@ -784,13 +796,13 @@ __global__ void __launch_bounds__(NTHREADS, 1) dense_fwd_kernel(const __grid_con
     fence_after();
     const uint32_t tmem = sh.tmem_base;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtrlRegs));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T::CTRL));
         if (warp == 0) copy_role<D, FEW>(p, maps, sh, lane);
         else if (warp < 3) mma_role<D, FEW>(p, sh, tmem, warp - 1, lane);
         else chunk_role<D>(p, sh, lane);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-        softmax_role<D, FEW>(p, sh, tmem, (warp - 4) >> 2, warp & 3, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T::SOFT));
+        softmax_role<D, FEW>(p, sh, tmem, (warp - 4) / T::SOFT_WARPS, (warp >> 2) % T::SPLIT, warp & 3, lane);
     }
     __syncwarp();
     fence_before();
@@ -832,18 +844,18 @@ __device__ __forceinline__ void join_add(Joined<D> &j, const float *o, const flo
         j.m = mn;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) j.o[e] *= a;
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float w = __shfl_sync(0xffffffffu, wt, i);
-            const float *src = o + row_of(k0 + i) * D;
-            if (w == 0.f) continue;                    // its row may never have been written
-            if constexpr (D == 64) {
-                const float2 y = *reinterpret_cast<const float2 *>(src + 2 * lane);
-                j.o[0] = fmaf(y.x, w, j.o[0]), j.o[1] = fmaf(y.y, w, j.o[1]);
-            } else {
-                const float4 y = *reinterpret_cast<const float4 *>(src + 4 * lane);
-                j.o[0] = fmaf(y.x, w, j.o[0]), j.o[1] = fmaf(y.y, w, j.o[1]);
-                j.o[2] = fmaf(y.z, w, j.o[2]), j.o[3] = fmaf(y.w, w, j.o[3]);
+        for (int i0 = 0; i0 < n; i0 += 8) {            // eight rows' loads together
+            using V = typename std::conditional<D == 64, float2, float4>::type;
+            V y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i < n) y[i] = __ldg(reinterpret_cast<const V *>(o + row_of(k0 + i0 + i) * D) + lane);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float w = i0 + i < n ? __shfl_sync(0xffffffffu, wt, i0 + i) : 0.f;
+                if (w == 0.f) continue;                // its row may never have been written
+                j.o[0] = fmaf(y[i].x, w, j.o[0]), j.o[1] = fmaf(y[i].y, w, j.o[1]);
+                if constexpr (D == 128) j.o[2] = fmaf(y[i].z, w, j.o[2]), j.o[3] = fmaf(y[i].w, w, j.o[3]);
             }
         }
     }
@@ -962,6 +974,7 @@ __global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ 
 // ---------------------------------------------------------------- host
 
 template <int D, bool FEW> cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, const FwdParams &p, cudaStream_t stream) {
+    using T = Threads<D, FEW>;
     Maps maps;
     const FwdSet &s = p.plan.s;
     const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)pb.rows, (cuuint64_t)pb.kv_heads, (cuuint64_t)pb.batch};
@@ -975,9 +988,10 @@ template <int D, bool FEW> cudaError_t launch(const DenseProblem &pb, const void
         return cudaErrorInvalidValue;
     const size_t smem = sizeof(Shared<D>) + 1024;
     static_assert(sizeof(Shared<D>) + 1024 <= 232448, "shared memory");
-    const cudaError_t e = kernel_ready<dense_fwd_kernel<D, FEW>>(smem, NTHREADS, kRegsNeeded);
+    static_assert(FEW || sizeof(Shared<D>::merge) >= 2048 * 2 * T::SOFT_WARPS, "staging of the epilogue");
+    const cudaError_t e = kernel_ready<dense_fwd_kernel<D, FEW>>(smem, T::ALL, T::REGS);
     if (e != cudaSuccess) return e;
-    dense_fwd_kernel<D, FEW><<<p.plan.ctas, NTHREADS, smem, stream>>>(maps, p);
+    dense_fwd_kernel<D, FEW><<<p.plan.ctas, T::ALL, smem, stream>>>(maps, p);
     return cudaGetLastError();
 }
 template <int D> cudaError_t run(const DenseProblem &pb, const void *q, const KeySet *sets, int nsets, FwdParams *p, cudaStream_t stream) {

@@ -131,6 +131,58 @@ __device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t *u) {
         : "memory");
 }
 
+// 64 bytes of each of a warp's 32 rows to global memory: lane l brings its row's 16 words and its address.
+// Through 2 KB of shared memory (16-byte pieces exchanged so that neither side meets bank conflicts), so
+// that four lanes write one row's 64 bytes together: with each lane writing its own row, every store
+// touches 32 lines, and an epilogue of 128 rows of 128 floats took 10,000 clocks.
+__device__ __forceinline__ void store_rows(uint8_t *stage, const uint32_t (&w)[16], void *dst, bool valid, int lane) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4 *>(stage + 64 * lane + 16 * (c ^ ((lane >> 1) & 3))) =
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+    __syncwarp();
+    const unsigned rows = __ballot_sync(0xffffffffu, valid);
+    const int c = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = 8 * i + (lane >> 2);
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + 64 * r + 16 * (c ^ ((r >> 1) & 3)));
+        char *to = reinterpret_cast<char *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(dst), r));
+        if ((rows >> r) & 1u) *reinterpret_cast<uint4 *>(to + 16 * c) = v;
+    }
+    __syncwarp();
+}
+// `cols` accumulator columns (a multiple of 32) of a warp's 32 rows, times f, to global memory: as bf16, or
+// as fp32 parts. dst: lane l's row. zero: the row is zeros whatever the accumulator holds. Not
+// inlined: an epilogue's registers would otherwise spill what the loop around it keeps.
+static __device__ __noinline__ void write_rows(uint8_t *stage, uint32_t taddr, int cols, float f, bool zero, bool bf16, void *dst,
+                                        bool valid, int lane) {
+#pragma unroll 1
+    for (int cc = 0; cc < cols; cc += 32) {
+        float o[32];
+        tmem_ld32(taddr + cc, o);
+        tmem_wait_ld_of(o);
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = zero ? 0.f : o[e] * f;
+        uint32_t w[16];
+        if (bf16) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+            store_rows(stage, w, static_cast<char *>(dst) + 2 * cc, valid, lane);
+        } else {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(o[16 * h + e]);
+                store_rows(stage, w, static_cast<char *>(dst) + 4 * (cc + 16 * h), valid, lane);
+            }
+        }
+    }
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // ---- host
 
 inline bool make_map(CUtensorMap *map, const void *base, int rank, const cuuint64_t *dims, const cuuint64_t *strides,
