@@ -85,6 +85,18 @@ struct Cut {
 struct FwdLayout {
     size_t part_o, part_lse, cuts, whole_o, whole_lse, spans, total;
 };
+// How `units` of `steps` each go to the CTAs: p.stream and p.ctas. Cutting units gives every CTA the same
+// number of steps, but its parts are written in fp32 (up to 256 rows a CTA, 38 MB at D = 128) and
+// joined by a kernel: together 8 to 12 us, about six steps of 1.5 to 2.3 us (few rows: four of 1.0 to
+// 1.3 us). So it is done where whole units would leave the busiest CTA with more steps than that.
+// Measured at 96 units of up to 7 steps (six padded entries of 333 x 3 rows, D = 128): cut 33 us, whole
+// units 24. `scan`: the lengths are few enough for a warp to add up at each CTA's start.
+inline void deal(FwdPlan &p, int64_t units, int64_t steps, bool scan) {
+    const int64_t rounds = (units + kCtas - 1) / kCtas, share = (units * steps + kCtas - 1) / kCtas;
+    p.stream = scan && rounds * steps > (share > 2 ? share : 2) + (p.s.few ? 4 : 6);
+    const int64_t want = p.stream ? (units * steps + 1) / 2 : units;
+    p.ctas = (int32_t)(want < kCtas ? want : kCtas);
+}
 FwdPlan make_fwd_plan(const DenseProblem &p, const KeySet &set);
 FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d, bool two_sets);
 

@@ -701,13 +701,6 @@ struct BwdPlans {
     size_t stat, key_part, qry_part, key_cuts, qry_cuts, total;
 };
 
-// Equal shares of steps, or whole units a CTA where units have few steps or are very many.
-void deal(FwdPlan &p, int64_t units, int64_t steps, bool scan) {
-    p.stream = scan && steps > 4 && units < 16 * kCtas;
-    const int64_t want = p.stream ? (units * steps + 1) / 2 : units;
-    p.ctas = (int32_t)(want < kCtas ? want : kCtas);
-}
-
 BwdPlans make_plans(const DenseProblem &p, const KeySet &ks) {
     BwdPlans r{};
     const bool scan = !ks.len || ks.sets <= 1024;

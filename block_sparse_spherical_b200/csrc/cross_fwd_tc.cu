@@ -1033,11 +1033,7 @@ FwdPlan make_fwd_plan(const DenseProblem &p, const KeySet &ks) {
     s.pairs = (s.tiles + 1) / 2;
     s.upz = p.kv_heads * s.pairs;
     const int64_t t = (ks.n + kTile - 1) / kTile, units = s.sets * s.upz;
-    // Units of a few steps each, or very many of them, go whole to the CTAs: cutting would save less
-    // than the join costs. The scan of the lengths is a warp's work at a kernel's start.
-    r.stream = t > 4 && units < 16 * kCtas && (!ks.len || ks.sets <= 1024);
-    const int64_t want = r.stream ? (units * t + 1) / 2 : units;
-    r.ctas = (int32_t)(want < kCtas ? want : kCtas);
+    deal(r, units, t, !ks.len || ks.sets <= 1024);
     return r;
 }
 
