@@ -117,9 +117,12 @@ struct FwdParams {
     Cut *cuts;              // [ctas]: single set
     int2 *spans;            // [units]: two sets: first and last CTA of a unit
     int64_t all_rows;       // batch * kv_heads * rows
+    int cta0;               // first block of this pass in its launch
     float scale_log2;
     uint32_t *status;       // nullable
 };
+
+__device__ __forceinline__ int this_cta(const FwdParams &p) { return (int)blockIdx.x - p.cta0; }
 
 struct Maps {
     CUtensorMap q, k, v;
@@ -129,10 +132,10 @@ struct Maps {
 __device__ __forceinline__ Walk walk_begin(const FwdParams &p, int lane) {
     Walk w{};
     if (p.plan.stream) {
-        if (lane == 0 && p.cuts) p.cuts[blockIdx.x].last = -1;   // until one is noted
+        if (lane == 0 && p.cuts) p.cuts[this_cta(p)].last = -1;   // until one is noted
         w.total = total_steps(p.plan, lane);
-        w.at = cta_first(blockIdx.x, w.total, p.plan.ctas);
-        w.left = cta_first(blockIdx.x + 1, w.total, p.plan.ctas) - w.at;
+        w.at = cta_first(this_cta(p), w.total, p.plan.ctas);
+        w.left = cta_first(this_cta(p) + 1, w.total, p.plan.ctas) - w.at;
         if (w.left > 0) {
             const StepAt at = step_at(p.plan, w.at, lane);
             w.t = at.t;
@@ -141,7 +144,7 @@ __device__ __forceinline__ Walk walk_begin(const FwdParams &p, int lane) {
             w.uu = at.uu;
         }
     } else {
-        w.left = blockIdx.x;
+        w.left = this_cta(p);
     }
     return w;
 }
@@ -166,9 +169,9 @@ __device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c,
         steps = (int)min((int64_t)(w.steps - w.t), w.left);
         c.slot = steps == w.steps ? -1 : (w.t > 0 ? 0 : 1);
         if (lead && w.t == 0) {
-            const int last = c.slot < 0 ? (int)blockIdx.x : cta_of(w.at + w.steps - 1, w.total, p.plan.ctas);
-            if (p.spans) p.spans[w.z * s.upz + w.uu] = make_int2(blockIdx.x, last);
-            else if (c.slot == 1) p.cuts[blockIdx.x] = Cut{(int)c.z, (int)c.hk, (int)c.pair, last};
+            const int last = c.slot < 0 ? this_cta(p) : cta_of(w.at + w.steps - 1, w.total, p.plan.ctas);
+            if (p.spans) p.spans[w.z * s.upz + w.uu] = make_int2(this_cta(p), last);
+            else if (c.slot == 1) p.cuts[this_cta(p)] = Cut{(int)c.z, (int)c.hk, (int)c.pair, last};
         }
         w.t += steps;
         w.at += steps;
@@ -184,7 +187,7 @@ __device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c,
         c.t0 = 0;
         c.slot = -1;
         steps = 0x7fffffff;
-        w.left += gridDim.x;
+        w.left += p.plan.ctas;
     }
     const int len = set_len(s.len, c.z, s.n, lead ? p.status : nullptr), tiles = (len + kTile - 1) / kTile;
     c.nt = min(steps, tiles - c.t0);                   // 0 for a set without keys
@@ -485,7 +488,7 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
     r.bf16 = c.slot < 0 && !p.whole_o;
     if (!r.valid) return r;
     if (c.slot >= 0) {
-        const int64_t at = (2 * (int64_t)blockIdx.x + c.slot) * (2 * kTile) + i_unit;
+        const int64_t at = (2 * (int64_t)this_cta(p) + c.slot) * (2 * kTile) + i_unit;
         r.o32 = p.part_o + at * D;
         r.lse = p.part_lse + at;
     } else if (p.whole_o) {
@@ -748,9 +751,9 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
     }
 }
 
-template <int D, bool FEW>
-__global__ void __launch_bounds__((Threads<D, FEW>::ALL), 1) dense_fwd_kernel(const __grid_constant__ Maps maps,
-                                                                const __grid_constant__ FwdParams p) {
+// One CTA of a pass. L: the threads and registers of the launch (a few-rows pass may share one of more
+// threads; the warps beyond its own idle).
+template <int D, bool FEW, typename L> __device__ __forceinline__ void fwd_cta(const Maps &maps, const FwdParams &p) {
     using T = Threads<D, FEW>;
     extern __shared__ uint8_t smem_raw[];
     Shared<D> &sh = *reinterpret_cast<Shared<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -796,13 +799,13 @@ __global__ void __launch_bounds__((Threads<D, FEW>::ALL), 1) dense_fwd_kernel(co
     fence_after();
     const uint32_t tmem = sh.tmem_base;
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(T::CTRL));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::CTRL));
         if (warp == 0) copy_role<D, FEW>(p, maps, sh, lane);
         else if (warp < 3) mma_role<D, FEW>(p, sh, tmem, warp - 1, lane);
         else chunk_role<D>(p, sh, lane);
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(T::SOFT));
-        softmax_role<D, FEW>(p, sh, tmem, (warp - 4) / T::SOFT_WARPS, (warp >> 2) % T::SPLIT, warp & 3, lane);
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::SOFT));
+        if (warp < 4 + 2 * T::SOFT_WARPS) softmax_role<D, FEW>(p, sh, tmem, (warp - 4) / T::SOFT_WARPS, (warp >> 2) % T::SPLIT, warp & 3, lane);
     }
     __syncwarp();
     fence_before();
@@ -811,6 +814,22 @@ __global__ void __launch_bounds__((Threads<D, FEW>::ALL), 1) dense_fwd_kernel(co
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+}
+
+template <int D, bool FEW>
+__global__ void __launch_bounds__((Threads<D, FEW>::ALL), 1) dense_fwd_kernel(const __grid_constant__ Maps maps,
+                                                                const __grid_constant__ FwdParams p) {
+    fwd_cta<D, FEW, Threads<D, FEW>>(maps, p);
+}
+// Two sets in one launch, the first set's CTAs first: the second's begin on each SM as the first's end there.
+template <int D, bool FEW0, bool FEW1>
+__global__ void __launch_bounds__((Threads<D, FEW0>::ALL), 1)
+dense_fwd_pair_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ FwdParams p0, const __grid_constant__ Maps maps1,
+                      const __grid_constant__ FwdParams p1) {
+    using L = Threads<D, FEW0>;
+    static_assert(L::ALL >= Threads<D, FEW1>::ALL, "threads of the launch");
+    if ((int)blockIdx.x < p1.cta0) fwd_cta<D, FEW0, L>(maps0, p0);
+    else fwd_cta<D, FEW1, L>(maps1, p1);
 }
 
 // ---------------------------------------------------------------- join
@@ -936,76 +955,165 @@ template <int D> __global__ void __launch_bounds__(256) join_cut_kernel(const __
     }
 }
 
-// Two sets: a warp joins one row's parts of both.
+// Two sets: a warp joins two rows' parts of both. Where no unit is cut into more than four, all their loads
+// go out together.
+constexpr int kSetRows = 2;
 template <int D>
 __global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ FwdParams p0, const __grid_constant__ FwdParams p1) {
-    const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
-    const int64_t row = (int64_t)blockIdx.x * 8 + warp;
-    if (row >= p0.all_rows) return;
-    // 32-bit divisions where they do: rows of a slab, members and tiles of a set are far below 2^31
-    const uint32_t slab = (uint32_t)(row / p0.plan.rows), b = slab / (uint32_t)p0.plan.kv_heads;
-    const uint32_t r = (uint32_t)(row - (int64_t)slab * p0.plan.rows), hk = slab - b * (uint32_t)p0.plan.kv_heads;
-    Joined<D> j;
-    join_begin<D>(j);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-        const FwdParams &p = k ? p1 : p0;
+    using V = typename std::conditional<D == 64, float2, float4>::type;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t row0 = ((int64_t)blockIdx.x * 8 + warp) * kSetRows;
+    // lane 2r + k: where row r's parts of set k are: parts from CTA ca on at row i of a unit, or one whole row
+    int count = 0, ca = 0, at = 0;
+    if (lane < 2 * kSetRows && row0 + (lane >> 1) < p0.all_rows) {
+        const FwdParams &p = lane & 1 ? p1 : p0;
         const FwdSet &s = p.plan.s;
+        const int64_t row = row0 + (lane >> 1);
+        // 32-bit divisions where they do: rows of a slab, members and tiles of a set are far below 2^31
+        const uint32_t rows = (uint32_t)p.plan.rows, heads = (uint32_t)p.plan.kv_heads;
+        const uint32_t slab = (uint32_t)quotient(row, rows), r = (uint32_t)(row - (int64_t)slab * rows);
+        const uint32_t b = slab / heads, hk = slab - b * heads;
         const uint32_t z = b / (uint32_t)s.members, member = b - z * (uint32_t)s.members;
         uint32_t t, i;
         if (s.bb) {
             t = member / (uint32_t)s.bb;
-            i = (member - t * s.bb) * (uint32_t)p.plan.rows + r;
+            i = (member - t * s.bb) * rows + r;
         } else {
             t = member * s.tpm + r / kTile;
             i = r % kTile;
         }
         const int2 span = p.spans[z * s.upz + hk * s.pairs + t / 2];
         // (after an expired wait a span may be missing; what it holds then must not lead out of the parts)
-        if (span.x < 0 || span.y < span.x || span.y >= p.plan.ctas) continue;
-        if (span.x == span.y)
-            join_add<D>(j, p.whole_o, p.whole_lse, 1, [row](int) { return row; }, lane);
-        else
-            join_add<D>(j, p.part_o, p.part_lse, span.y - span.x + 1, PartRow{span.x, (int)(i + kTile * (t & 1))}, lane);
+        if (span.x >= 0 && span.y >= span.x && span.y < p.plan.ctas) {
+            count = span.y - span.x + 1;
+            ca = span.x;
+            at = (int)(i + kTile * (t & 1));
+        }
     }
-    join_store<D>(j, p0.out, nullptr, row, lane);
+    const int most = __reduce_max_sync(0xffffffffu, count);
+    if (most <= kJoinParts) {
+        V y[kSetRows][2][kJoinParts];
+        float ls[kSetRows][2][kJoinParts];
+#pragma unroll
+        for (int r = 0; r < kSetRows; ++r)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const FwdParams &p = k ? p1 : p0;
+                const int n = __shfl_sync(0xffffffffu, count, 2 * r + k), c = __shfl_sync(0xffffffffu, ca, 2 * r + k);
+                const PartRow part{c, __shfl_sync(0xffffffffu, at, 2 * r + k)};
+#pragma unroll
+                for (int j = 0; j < kJoinParts; ++j) {
+                    ls[r][k][j] = -CUDART_INF_F;
+                    if (j < n) {
+                        const int64_t from = n == 1 ? row0 + r : part(j);
+                        ls[r][k][j] = __ldg((n == 1 ? p.whole_lse : p.part_lse) + from);
+                        y[r][k][j] = __ldg(reinterpret_cast<const V *>((n == 1 ? p.whole_o : p.part_o) + from * D) + lane);
+                    }
+                }
+            }
+#pragma unroll
+        for (int r = 0; r < kSetRows; ++r) {
+            if (row0 + r >= p0.all_rows) continue;
+            Joined<D> j;
+            join_begin<D>(j);
+#pragma unroll
+            for (int k = 0; k < 2 * kJoinParts; ++k) j.m = fmaxf(j.m, ls[r][k / kJoinParts][k % kJoinParts]);
+#pragma unroll
+            for (int k = 0; k < 2 * kJoinParts; ++k) {
+                const float l = ls[r][k / kJoinParts][k % kJoinParts];
+                if (l == -CUDART_INF_F) continue;
+                const V v = y[r][k / kJoinParts][k % kJoinParts];
+                const float w = ex2(l - j.m);
+                j.l += w;
+                j.o[0] = fmaf(v.x, w, j.o[0]), j.o[1] = fmaf(v.y, w, j.o[1]);
+                if constexpr (D == 128) j.o[2] = fmaf(v.z, w, j.o[2]), j.o[3] = fmaf(v.w, w, j.o[3]);
+            }
+            join_store<D>(j, p0.out, nullptr, row0 + r, lane);
+        }
+        return;
+    }
+    for (int r = 0; r < kSetRows; ++r) {
+        const int64_t row = row0 + r;
+        if (row >= p0.all_rows) return;
+        Joined<D> j;
+        join_begin<D>(j);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const FwdParams &p = k ? p1 : p0;
+            const int n = __shfl_sync(0xffffffffu, count, 2 * r + k), c = __shfl_sync(0xffffffffu, ca, 2 * r + k);
+            const int i = __shfl_sync(0xffffffffu, at, 2 * r + k);
+            if (n == 1) join_add<D>(j, p.whole_o, p.whole_lse, 1, [row](int) { return row; }, lane);
+            else join_add<D>(j, p.part_o, p.part_lse, n, PartRow{c, i}, lane);
+        }
+        join_store<D>(j, p0.out, nullptr, row, lane);
+    }
 }
 
 // ---------------------------------------------------------------- host
 
-template <int D, bool FEW> cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, const FwdParams &p, cudaStream_t stream) {
-    using T = Threads<D, FEW>;
-    Maps maps;
-    const FwdSet &s = p.plan.s;
-    const cuuint64_t qd[4] = {(cuuint64_t)D, (cuuint64_t)pb.rows, (cuuint64_t)pb.kv_heads, (cuuint64_t)pb.batch};
-    const cuuint64_t qs[3] = {(cuuint64_t)D * 2, (cuuint64_t)pb.rows * D * 2, (cuuint64_t)pb.kv_heads * pb.rows * D * 2};
-    const cuuint32_t qb[4] = {64, s.bb ? (cuuint32_t)pb.rows : (cuuint32_t)kTile, 1, s.bb ? (cuuint32_t)s.bb : 1u};
-    const cuuint64_t kd[3] = {(cuuint64_t)D, (cuuint64_t)ks.n, (cuuint64_t)(ks.sets * pb.kv_heads)};
-    const cuuint64_t kst[2] = {(cuuint64_t)D * 2, (cuuint64_t)ks.n * D * 2};
+bool make_maps(Maps &maps, const DenseProblem &pb, const void *q, const KeySet &ks, const FwdSet &s) {
+    const cuuint64_t d = pb.d, rows = pb.rows, heads = pb.kv_heads, n = ks.n;
+    const cuuint64_t qd[4] = {d, rows, heads, (cuuint64_t)pb.batch}, qs[3] = {d * 2, rows * d * 2, heads * rows * d * 2};
+    const cuuint32_t qb[4] = {64, s.bb ? (cuuint32_t)rows : (cuuint32_t)kTile, 1, s.bb ? (cuuint32_t)s.bb : 1u};
+    const cuuint64_t kd[3] = {d, n, (cuuint64_t)ks.sets * heads}, kst[2] = {d * 2, n * d * 2};
     const cuuint32_t kb[3] = {64, kTile, 1};
-    if (!make_map(&maps.q, q, 4, qd, qs, qb) || !make_map(&maps.k, ks.k, 3, kd, kst, kb) ||
-        !make_map(&maps.v, ks.v, 3, kd, kst, kb))
-        return cudaErrorInvalidValue;
-    const size_t smem = sizeof(Shared<D>) + 1024;
-    static_assert(sizeof(Shared<D>) + 1024 <= 232448, "shared memory");
-    static_assert(FEW || sizeof(Shared<D>::merge) >= 2048 * 2 * T::SOFT_WARPS, "staging of the epilogue");
-    const cudaError_t e = kernel_ready<dense_fwd_kernel<D, FEW>>(smem, T::ALL, T::REGS);
+    return make_map(&maps.q, q, 4, qd, qs, qb) && make_map(&maps.k, ks.k, 3, kd, kst, kb) &&
+           make_map(&maps.v, ks.v, 3, kd, kst, kb);
+}
+template <int D> constexpr size_t kSmem = sizeof(Shared<D>) + 1024;
+static_assert(kSmem<64> <= 232448 && kSmem<128> <= 232448, "shared memory");
+static_assert(sizeof(Shared<64>::merge) >= 2048 * 2 * Threads<64, false>::SOFT_WARPS &&
+                  sizeof(Shared<128>::merge) >= 2048 * 2 * Threads<128, false>::SOFT_WARPS, "staging of the epilogue");
+
+template <int D, bool FEW> cudaError_t launch_one(const Maps &maps, const FwdParams &p, cudaStream_t stream) {
+    using T = Threads<D, FEW>;
+    const cudaError_t e = kernel_ready<dense_fwd_kernel<D, FEW>>(kSmem<D>, T::ALL, T::REGS);
     if (e != cudaSuccess) return e;
-    dense_fwd_kernel<D, FEW><<<p.plan.ctas, T::ALL, smem, stream>>>(maps, p);
+    dense_fwd_kernel<D, FEW><<<p.plan.ctas, T::ALL, kSmem<D>, stream>>>(maps, p);
+    return cudaGetLastError();
+}
+template <int D, bool FEW0, bool FEW1>
+cudaError_t launch_pair(const Maps *maps, FwdParams *p, cudaStream_t stream) {
+    using T = Threads<D, FEW0>;
+    const cudaError_t e = kernel_ready<dense_fwd_pair_kernel<D, FEW0, FEW1>>(kSmem<D>, T::ALL, T::REGS);
+    if (e != cudaSuccess) return e;
+    p[1].cta0 = p[0].plan.ctas;
+    dense_fwd_pair_kernel<D, FEW0, FEW1><<<p[0].plan.ctas + p[1].plan.ctas, T::ALL, kSmem<D>, stream>>>(maps[0], p[0], maps[1], p[1]);
     return cudaGetLastError();
 }
 template <int D> cudaError_t run(const DenseProblem &pb, const void *q, const KeySet *sets, int nsets, FwdParams *p, cudaStream_t stream) {
-    for (int k = 0; k < nsets; ++k) {
-        const cudaError_t e = p[k].plan.s.few ? launch<D, true>(pb, q, sets[k], p[k], stream)
-                                              : launch<D, false>(pb, q, sets[k], p[k], stream);
-        if (e != cudaSuccess) return e;
-    }
-    if (nsets == 2) {
-        join_sets_kernel<D><<<(unsigned)((p[0].all_rows + 7) / 8), 256, 0, stream>>>(p[0], p[1]);
-    } else if (p[0].cuts) {
+    Maps maps[2];
+    for (int k = 0; k < nsets; ++k)
+        if (!make_maps(maps[k], pb, q, sets[k], p[k].plan.s)) return cudaErrorInvalidValue;
+    cudaError_t e;
+    if (nsets == 1) {
+        e = p[0].plan.s.few ? launch_one<D, true>(maps[0], p[0], stream) : launch_one<D, false>(maps[0], p[0], stream);
+        if (e != cudaSuccess || !p[0].cuts) return e;
         const int each = p[0].plan.s.few ? 1 : kJoinRows, rows = p[0].plan.s.few ? kFewRows : 2 * kTile;
         join_cut_kernel<D><<<dim3(p[0].plan.ctas, rows / (8 * each)), 256, 0, stream>>>(p[0], each);
+        return cudaGetLastError();
     }
+    // the rows of a set are those of its members together: at least as many in the first set
+    const bool few0 = p[0].plan.s.few, few1 = p[1].plan.s.few;
+    if (few0 && !few1) return cudaErrorInvalidValue;
+    // Short passes share the SMs by their steps (and one for each unit's end); of long ones the second follows
+    // the first on each SM, which needs no guess of what a step of either costs.
+    int64_t work[2];
+    for (int k = 0; k < 2; ++k) {
+        const FwdSet &s = p[k].plan.s;
+        work[k] = s.sets * s.upz * ((s.n + kTile - 1) / kTile + 1);
+    }
+    if (p[0].plan.ctas + p[1].plan.ctas > kCtas && work[0] + work[1] < 16 * kCtas) {
+        const int64_t share = kCtas * work[0] / (work[0] + work[1]), c0 = share < 1 ? 1 : (share > kCtas - 1 ? kCtas - 1 : share);
+        if (p[0].plan.ctas > c0) p[0].plan.ctas = (int32_t)c0;
+        if (p[1].plan.ctas > kCtas - c0) p[1].plan.ctas = (int32_t)(kCtas - c0);
+    }
+    e = few0   ? launch_pair<D, true, true>(maps, p, stream)
+        : few1 ? launch_pair<D, false, true>(maps, p, stream)
+               : launch_pair<D, false, false>(maps, p, stream);
+    if (e != cudaSuccess) return e;
+    constexpr int rows = 8 * kSetRows;
+    join_sets_kernel<D><<<(unsigned)((p[0].all_rows + rows - 1) / rows), 256, 0, stream>>>(p[0], p[1]);
     return cudaGetLastError();
 }
 
