@@ -86,9 +86,9 @@ def load() -> ctypes.CDLL:
         "bsa_latlon_to_healpix": [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32,
                                   ctypes.c_float, P, P, P, P, P, P, P, S, P, P],
         "bsa_cross_workspace_size": [X, ctypes.POINTER(ctypes.c_size_t)],
-        "bsa_cross_attention": [X, P, P, P, P, P, P, P, S, P, P],
+        "bsa_cross_attention": [X, P, P, P, P, P, P, P, P, S, P, P],
         "bsa_cross_backward_workspace_size": [X, ctypes.POINTER(ctypes.c_size_t)],
-        "bsa_cross_attention_backward": [X, P, P, P, P, P, P, P, P, P, P, P, S, P, P],
+        "bsa_cross_attention_backward": [X, P, P, P, P, P, P, P, P, P, P, P, P, S, P, P],
         "bsa_prefix_workspace_size": [Y, ctypes.POINTER(ctypes.c_size_t)],
         "bsa_prefix_attention": [Y, P, P, P, P, P, P, P, P, P, S, P, P],
         "bsa_testing_fine_attention_withhold": [C, P, P, P, P, P, P, P, P, ctypes.c_int64, P],
@@ -239,11 +239,11 @@ def bsa_cross_workspace_size(cfg: BsaCrossConfig) -> int:
     return n.value
 
 
-def bsa_cross_attention(cfg: BsaCrossConfig, q, k, v, key_len, out, lse, workspace, workspace_bytes: int,
-                        status_word=None, stream=None) -> None:
+def bsa_cross_attention(cfg: BsaCrossConfig, q, k, v, key_len, out, lse, out_low, workspace,
+                        workspace_bytes: int, status_word=None, stream=None) -> None:
     _check("bsa_cross_attention", load().bsa_cross_attention(
-        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(key_len), _ptr(out), _ptr(lse), _ptr(workspace),
-        workspace_bytes, _ptr(status_word), _stream(stream)))
+        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(key_len), _ptr(out), _ptr(lse), _ptr(out_low),
+        _ptr(workspace), workspace_bytes, _ptr(status_word), _stream(stream)))
 
 
 def bsa_cross_backward_workspace_size(cfg: BsaCrossConfig) -> int:
@@ -253,11 +253,11 @@ def bsa_cross_backward_workspace_size(cfg: BsaCrossConfig) -> int:
     return n.value
 
 
-def bsa_cross_attention_backward(cfg: BsaCrossConfig, q, k, v, key_len, out, lse, dout, dq, dk, dv, workspace,
-                                 workspace_bytes: int, status_word=None, stream=None) -> None:
+def bsa_cross_attention_backward(cfg: BsaCrossConfig, q, k, v, key_len, out, lse, out_low, dout, dq, dk, dv,
+                                 workspace, workspace_bytes: int, status_word=None, stream=None) -> None:
     _check("bsa_cross_attention_backward", load().bsa_cross_attention_backward(
-        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(key_len), _ptr(out), _ptr(lse), _ptr(dout), _ptr(dq),
-        _ptr(dk), _ptr(dv), _ptr(workspace), workspace_bytes, _ptr(status_word), _stream(stream)))
+        ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(v), _ptr(key_len), _ptr(out), _ptr(lse), _ptr(out_low), _ptr(dout),
+        _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace), workspace_bytes, _ptr(status_word), _stream(stream)))
 
 
 def bsa_prefix_workspace_size(cfg: BsaPrefixConfig) -> int:

@@ -310,23 +310,24 @@ class CrossAttention(_DenseLayer):
         self.shape = (batch, heads, n_q, head_dim)
         self.kv_shape = (batch, self.kv_heads, n_k, head_dim)
 
-    def _forward(self, q, k, v, key_len, out, lse):
+    def _forward(self, q, k, v, key_len, out, lse=None, low=None):
         args = (self._take(q, "q", self.shape), self._take(k, "k", self.kv_shape), self._take(v, "v", self.kv_shape),
                 self._lengths(key_len, "key_len", self.batch))
         out, address = self._output(out, "out", self.shape, q)
-        self._run(abi.bsa_cross_attention, (*args, address, None if lse is None else lse.data_ptr()),
+        self._run(abi.bsa_cross_attention, (*args, address, *(None if t is None else t.data_ptr() for t in (lse, low))),
                   self.workspace_bytes)
         return out
 
     def __call__(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
-        return self._forward(q, k, v, key_len, out, None)
+        return self._forward(q, k, v, key_len, out)
 
 
 class CrossAttentionTrain(CrossAttention):
     """A CrossAttention layer for training.
 
     forward(q, k, v, key_len) -> out; backward(dout) -> (dq, dk, dv) of the last forward(). Its q, k, v,
-    key_len and out are kept by reference until then and have to stay as they are.
+    key_len and out are kept by reference until then and have to stay as they are (and with them, of
+    the layer's own, the rows' log-sum-exp and what rounding out to bf16 left off).
     """
 
     def __init__(self, *args, **kw):
@@ -339,8 +340,9 @@ class CrossAttentionTrain(CrossAttention):
 
     def forward(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
         lse = torch.empty(self.shape[:3], dtype=torch.float32, device=self.device)
-        out = self._forward(q, k, v, key_len, out, lse)
-        self._saved = (q, k, v, key_len, out, lse)
+        low = torch.empty(self.shape, dtype=self.dtype, device=self.device)
+        out = self._forward(q, k, v, key_len, out, lse, low)
+        self._saved = (q, k, v, key_len, out, lse, low)
         return out
 
     def backward(self, dout, grads=None):

@@ -101,11 +101,11 @@ FwdPlan make_fwd_plan(const DenseProblem &p, const KeySet &set);
 FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d, bool two_sets);
 
 // Launchers (return cudaGetLastError()).
-cudaError_t launch_dense_fwd(const DenseProblem &p, const void *q, const KeySet *sets, int nsets, void *out, float *lse,
+cudaError_t launch_dense_fwd(const DenseProblem &p, const void *q, const KeySet *sets, int nsets, void *out, void *low, float *lse,
                              float *workspace, uint32_t *status, cudaStream_t stream);
 size_t dense_bwd_floats(const DenseProblem &p, const KeySet &s);   // workspace of a backward pass
-cudaError_t launch_dense_bwd(const DenseProblem &p, const void *q, const KeySet &s, const void *out, const float *lse,
-                             const void *dout, void *dq, void *dk, void *dv, float *workspace, uint32_t *status,
+cudaError_t launch_dense_bwd(const DenseProblem &p, const void *q, const KeySet &s, const void *out, const void *low,
+                             const float *lse, const void *dout, void *dq, void *dk, void *dv, float *workspace, uint32_t *status,
                              cudaStream_t stream);
 
 #ifdef __CUDACC__

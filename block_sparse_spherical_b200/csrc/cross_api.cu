@@ -95,20 +95,22 @@ bsa_status bsa_cross_workspace_size(const bsa_cross_config *cfg, size_t *bytes) 
 }
 
 bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
-                               const int32_t *key_len, void *out, float *lse, void *workspace, size_t workspace_bytes,
-                               uint32_t *status_word, cudaStream_t stream) {
+                               const int32_t *key_len, void *out, float *lse, void *out_low, void *workspace,
+                               size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream) {
     DenseProblem p;
     const bsa_status st = make_cross(cfg, &p);
     if (st != BSA_OK) return st;
     if (!q || !k || !v || !out) return BSA_ERR_INVALID_ARG;
-    if (out == q || out == k || out == v) return BSA_ERR_INVALID_ARG;
+    for (const void *x : {q, k, v})
+        if (x == out || x == out_low) return BSA_ERR_INVALID_ARG;
+    if (out_low == out) return BSA_ERR_INVALID_ARG;
     const KeySet s = cross_set(cfg, k, v, key_len);
     const bsa_status ws = check_workspace(workspace, workspace_bytes, fwd_bytes(p, &s, 1));
     if (ws != BSA_OK) return ws;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
-        !aligned(key_len, 4) || !aligned(status_word, 4))
+        !aligned(out_low, 16) || !aligned(key_len, 4) || !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
-    return from_cuda(bsa::launch_dense_fwd(p, q, &s, 1, out, lse, static_cast<float *>(workspace), status_word, stream));
+    return from_cuda(bsa::launch_dense_fwd(p, q, &s, 1, out, out_low, lse, static_cast<float *>(workspace), status_word, stream));
 }
 
 bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t *bytes) {
@@ -121,9 +123,9 @@ bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t
 }
 
 bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
-                                        const int32_t *key_len, const void *out, const float *lse, const void *dout,
-                                        void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes,
-                                        uint32_t *status_word, cudaStream_t stream) {
+                                        const int32_t *key_len, const void *out, const float *lse, const void *out_low,
+                                        const void *dout, void *dq, void *dk, void *dv, void *workspace,
+                                        size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream) {
     DenseProblem p;
     const bsa_status st = make_cross(cfg, &p);
     if (st != BSA_OK) return st;
@@ -135,16 +137,17 @@ bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void 
         if (!grads[i] || grads[i] == grads[(i + 1) % 3]) return BSA_ERR_INVALID_ARG;
         for (const void *x : in)
             if (x == grads[i]) return BSA_ERR_INVALID_ARG;
+        if (grads[i] == out_low) return BSA_ERR_INVALID_ARG;
     }
     const KeySet s = cross_set(cfg, k, v, key_len);
     const bsa_status ws = check_workspace(workspace, workspace_bytes, bwd_bytes(p, s));
     if (ws != BSA_OK) return ws;
     for (int i = 0; i < 5; ++i)
         if (!aligned(in[i], 16)) return BSA_ERR_ALIGNMENT;
-    if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4) || !aligned(key_len, 4) ||
+    if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(out_low, 16) || !aligned(lse, 4) || !aligned(key_len, 4) ||
         !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
-    return from_cuda(bsa::launch_dense_bwd(p, q, s, out, lse, dout, dq, dk, dv, static_cast<float *>(workspace), status_word,
+    return from_cuda(bsa::launch_dense_bwd(p, q, s, out, out_low, lse, dout, dq, dk, dv, static_cast<float *>(workspace), status_word,
                                            stream));
 }
 
@@ -179,7 +182,7 @@ bsa_status bsa_prefix_attention(const bsa_prefix_config *cfg, const void *q, con
     if (!aligned(out, 16) || !aligned(prefix_len, 4) || !aligned(own_len, 4) || !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
     return from_cuda(
-        bsa::launch_dense_fwd(p, q, sets, 2, out, nullptr, static_cast<float *>(workspace), status_word, stream));
+        bsa::launch_dense_fwd(p, q, sets, 2, out, nullptr, nullptr, static_cast<float *>(workspace), status_word, stream));
 }
 
 }  // extern "C"

@@ -78,7 +78,8 @@ struct BwdMaps {
 // and zeros for the gradients of keys behind a length. D/8 lanes a row, 16 bytes each.
 template <int D>
 __global__ void __launch_bounds__(256) bwd_stat_kernel(const __grid_constant__ BwdParams p, const __nv_bfloat16 *out,
-                                                       const float *lse, const __nv_bfloat16 *dout, float *stat,
+                                                       const __nv_bfloat16 *low, const float *lse,
+                                                       const __nv_bfloat16 *dout, float *stat,
                                                        int64_t slabs) {
     constexpr int L = D / 8;
     const int sub = threadIdx.x % L;
@@ -92,11 +93,13 @@ __global__ void __launch_bounds__(256) bwd_stat_kernel(const __grid_constant__ B
             const int64_t at = slab * p.plan.rows + r;
             const uint4 a = __ldg(reinterpret_cast<const uint4 *>(out + at * D) + sub);
             const uint4 b = __ldg(reinterpret_cast<const uint4 *>(dout + at * D) + sub);
-            const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w};
+            const uint4 c = low ? __ldg(reinterpret_cast<const uint4 *>(low + at * D) + sub) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t ua[4] = {a.x, a.y, a.z, a.w}, ub[4] = {b.x, b.y, b.z, b.w}, uc[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                d = fmaf(__uint_as_float(ua[e] << 16), __uint_as_float(ub[e] << 16), d);
-                d = fmaf(__uint_as_float(ua[e] & 0xffff0000u), __uint_as_float(ub[e] & 0xffff0000u), d);
+                d = fmaf(__uint_as_float(ua[e] << 16) + __uint_as_float(uc[e] << 16), __uint_as_float(ub[e] << 16), d);
+                d = fmaf(__uint_as_float(ua[e] & 0xffff0000u) + __uint_as_float(uc[e] & 0xffff0000u),
+                         __uint_as_float(ub[e] & 0xffff0000u), d);
             }
             x = __ldg(lse + at) * 1.4426950408889634f;
             if (x == -CUDART_INF_F) x = CUDART_INF_F;
@@ -562,7 +565,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
             const int ub = (u + C::UB - 1) % C::UB;
             uint8_t *stage = (4 * w + wq < 8 ? sh.a0[ub] : sh.a1[ub]) + 2048 * ((4 * w + wq) & 7);
             write_rows(stage, tw + col + c0, wide, grad == 0 ? 1.f : p.scale, false, slot < 0,
-                       slot < 0 ? static_cast<void *>(d16 + c0) : d32 + c0, counts, lane);
+                       slot < 0 ? static_cast<void *>(d16 + c0) : d32 + c0, nullptr, counts, lane);
         } else if (!KEY && c0 < D && counts) {         // no keys: zeros (and the unit has no tiles here)
             for (int e = 0; e < 4; ++e) reinterpret_cast<uint4 *>(d16 + c0)[e] = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -744,8 +747,8 @@ bool row_map(CUtensorMap *m, const void *base, int64_t d, int64_t rows, int64_t 
 }
 
 template <int D>
-cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, const void *out, const float *lse,
-                   const void *dout, const BwdPlans &plans, const BwdParams &key, const BwdParams &qry, float *stat,
+cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, const void *out, const void *low,
+                   const float *lse, const void *dout, const BwdPlans &plans, const BwdParams &key, const BwdParams &qry, float *stat,
                    cudaStream_t stream) {
     const int64_t slabs = pb.batch * pb.kv_heads;
     BwdMaps mk, mq;
@@ -763,7 +766,7 @@ cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, cons
     if (e != cudaSuccess) return e;
     const int64_t rows_a_block = 256 / (D / 8), stat_blocks = (slabs * plans.qtiles * kTile + rows_a_block - 1) / rows_a_block;
     bwd_stat_kernel<D><<<(unsigned)(stat_blocks < 8 * kCtas ? stat_blocks : 8 * kCtas), 256, 0, stream>>>(
-        key, static_cast<const __nv_bfloat16 *>(out), lse, static_cast<const __nv_bfloat16 *>(dout), stat, slabs);
+        key, static_cast<const __nv_bfloat16 *>(out), static_cast<const __nv_bfloat16 *>(low), lse, static_cast<const __nv_bfloat16 *>(dout), stat, slabs);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     bwd_kernel<D, true><<<key.plan.ctas, NTHREADS, smem, stream>>>(mk, key);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -779,8 +782,8 @@ cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, cons
 
 size_t dense_bwd_floats(const DenseProblem &p, const KeySet &s) { return make_plans(p, s).total; }
 
-cudaError_t launch_dense_bwd(const DenseProblem &pb, const void *q, const KeySet &ks, const void *out, const float *lse,
-                             const void *dout, void *dq, void *dk, void *dv, float *ws, uint32_t *status,
+cudaError_t launch_dense_bwd(const DenseProblem &pb, const void *q, const KeySet &ks, const void *out, const void *low,
+                             const float *lse, const void *dout, void *dq, void *dk, void *dv, float *ws, uint32_t *status,
                              cudaStream_t stream) {
     const BwdPlans plans = make_plans(pb, ks);
     BwdParams key{};
@@ -800,8 +803,8 @@ cudaError_t launch_dense_bwd(const DenseProblem &pb, const void *q, const KeySet
     qry.part = ws + plans.qry_part;
     qry.cuts = plans.qry.stream ? reinterpret_cast<Cut *>(ws + plans.qry_cuts) : nullptr;
     float *stat = ws + plans.stat;
-    return pb.d == 64 ? launch<64>(pb, q, ks, out, lse, dout, plans, key, qry, stat, stream)
-                      : launch<128>(pb, q, ks, out, lse, dout, plans, key, qry, stat, stream);
+    return pb.d == 64 ? launch<64>(pb, q, ks, out, low, lse, dout, plans, key, qry, stat, stream)
+                      : launch<128>(pb, q, ks, out, low, lse, dout, plans, key, qry, stat, stream);
 }
 
 }  // namespace bsa

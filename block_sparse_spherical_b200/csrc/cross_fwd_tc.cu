@@ -111,7 +111,7 @@ template <int D> struct alignas(1024) Shared {
 
 struct FwdParams {
     FwdPlan plan;
-    __nv_bfloat16 *out;     // [rows of all][D]
+    __nv_bfloat16 *out, *low;   // [rows of all][D]; low: what rounding out leaves off, nullable
     float *lse;             // nullable
     float *part_o, *part_lse, *whole_o, *whole_lse;     // whole: null for a single set
     Cut *cuts;              // [ctas]: single set
@@ -472,7 +472,7 @@ __device__ __forceinline__ void numerators(const float *s, float sl2, float neg_
 
 // Where row i (of the unit's 256) of a chunk goes: out and lse, a part, or a whole row of a set.
 struct RowOut {
-    __nv_bfloat16 *o16;
+    __nv_bfloat16 *o16, *low;
     float *o32, *lse;
     float lse_unit;         // lse is kept in log2 units in the workspace, given out in natural ones
     bool valid, bf16;       // bf16: o16, for all rows of the chunk
@@ -482,7 +482,7 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
     RowOut r;
     const int64_t row = plan_row(p.plan, c.z, c.hk, tile, i_tile);
     r.valid = row >= 0;
-    r.o16 = nullptr;
+    r.o16 = r.low = nullptr;
     r.o32 = r.lse = nullptr;
     r.lse_unit = 1.f;
     r.bf16 = c.slot < 0 && !p.whole_o;
@@ -497,6 +497,7 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
         r.lse = p.whole_lse + at;
     } else {
         r.o16 = p.out + row * D;
+        r.low = p.low ? p.low + row * D : nullptr;
         r.lse = p.lse ? p.lse + row : nullptr;
         r.lse_unit = kLn2;
     }
@@ -532,8 +533,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
 #pragma unroll 1
             for (int cc = COLS * hh; cc < COLS * (hh + 1); cc += 16) {
                 uint32_t o[16];
-                tmem_ld16w(tO + cc, o);
-                tmem_wait_ld();
+                tmem_ld16_now(tO + cc, o);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                 tmem_st16w(tO + cc, o);
@@ -636,7 +636,8 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
             const float inv = l == 0.f ? 0.f : 1.f / l;
             uint8_t *stage = reinterpret_cast<uint8_t *>(sh.merge) + 2048 * (4 * (SPLIT * pl + hh) + wq);
             void *dst = r.bf16 ? static_cast<void *>(r.o16 + COLS * hh) : r.o32 + COLS * hh;
-            write_rows(stage, tO + COLS * hh, COLS, inv, n == 0 || l == 0.f, r.bf16, dst, r.valid, lane);
+            write_rows(stage, tO + COLS * hh, COLS, inv, n == 0 || l == 0.f, r.bf16, dst,
+                       r.low ? r.low + COLS * hh : nullptr, r.valid, lane);
             if (hh == 0 && r.valid && r.lse) *r.lse = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * r.lse_unit;
             fence_before();
             chunk_done<D>(sh, i, lane);
@@ -649,7 +650,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
             fence_after();
             float x[32];
             tmem_ld32(tS + 32 * wq, x);
-            tmem_wait_ld();
+            tmem_wait_ld_of(x);
             fence_before();
             warp_arrive(&sh.s_free[pl], lane);
             const int valid = rel - t * kTile - 32 * wq;
@@ -702,7 +703,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 float o[32];
                 if (any) {
                     tmem_ld32(tO + 32 * cc, o);
-                    tmem_wait_ld();
+                    tmem_wait_ld_of(o);
                 }
                 if (mine) {
                     float4 *dst = reinterpret_cast<float4 *>(&sh.merge[idx][lane - r0][32 * cc]);
@@ -729,10 +730,15 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                     }
                     const RowOut r = row_out<D>(p, *cp, 0, r0 + mr, r0 + mr);
                     if (r.valid) {
-                        if (r.o16)
-                            *reinterpret_cast<uint2 *>(r.o16 + col) = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-                        else
+                        if (r.o16) {
+                            const uint2 u = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+                            *reinterpret_cast<uint2 *>(r.o16 + col) = u;
+                            if (r.low)
+                                *reinterpret_cast<uint2 *>(r.low + col) =
+                                    make_uint2(rest_bf16x2(y.x, y.y, u.x), rest_bf16x2(y.z, y.w, u.y));
+                        } else {
                             *reinterpret_cast<float4 *>(r.o32 + col) = y;
+                        }
                     }
                 }
             }
@@ -880,14 +886,23 @@ __device__ __forceinline__ void join_add(Joined<D> &j, const float *o, const flo
     }
 }
 template <int D>
-__device__ __forceinline__ void join_store(const Joined<D> &j, __nv_bfloat16 *out, float *lse, int64_t row, int lane) {
+__device__ __forceinline__ void join_store(const Joined<D> &j, const FwdParams &p, int64_t row, int lane) {
+    using V = typename std::conditional<D == 64, uint32_t, uint2>::type;
     const float inv = j.l == 0.f ? 0.f : 1.f / j.l;
-    uint32_t u[D / 64];
+    uint32_t u[D / 64], low[D / 64];
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) u[e] = pack_bf16x2(j.o[2 * e] * inv, j.o[2 * e + 1] * inv);
-    if constexpr (D == 64) reinterpret_cast<uint32_t *>(out + row * D)[lane] = u[0];
-    else reinterpret_cast<uint2 *>(out + row * D)[lane] = make_uint2(u[0], u[1]);
-    if (lse && lane == 0) lse[row] = j.l == 0.f ? -CUDART_INF_F : (j.m + __log2f(j.l)) * kLn2;
+    for (int e = 0; e < D / 64; ++e) {
+        const float a = j.o[2 * e] * inv, b = j.o[2 * e + 1] * inv;
+        u[e] = pack_bf16x2(a, b);
+        low[e] = rest_bf16x2(a, b, u[e]);
+    }
+    auto put = [&](__nv_bfloat16 *to, const uint32_t *w) {
+        if constexpr (D == 64) reinterpret_cast<V *>(to + row * D)[lane] = w[0];
+        else reinterpret_cast<V *>(to + row * D)[lane] = make_uint2(w[0], w[1]);
+    };
+    put(p.out, u);
+    if (p.low) put(p.low, low);
+    if (p.lse && lane == 0) p.lse[row] = j.l == 0.f ? -CUDART_INF_F : (j.m + __log2f(j.l)) * kLn2;
 }
 // Row i (of a unit's 256) of the parts that CTA ca begins: number of the k-th part's row.
 struct PartRow {
@@ -941,7 +956,7 @@ template <int D> __global__ void __launch_bounds__(256) join_cut_kernel(const __
                 j.o[0] = fmaf(y[r][k].x, w, j.o[0]), j.o[1] = fmaf(y[r][k].y, w, j.o[1]);
                 if constexpr (D == 128) j.o[2] = fmaf(y[r][k].z, w, j.o[2]), j.o[3] = fmaf(y[r][k].w, w, j.o[3]);
             }
-            join_store<D>(j, p.out, p.lse, row, lane);
+            join_store<D>(j, p, row, lane);
         }
         return;
     }
@@ -951,7 +966,7 @@ template <int D> __global__ void __launch_bounds__(256) join_cut_kernel(const __
         Joined<D> j;
         join_begin<D>(j);
         join_add<D>(j, p.part_o, p.part_lse, count, PartRow{ca, i}, lane);
-        join_store<D>(j, p.out, p.lse, row, lane);
+        join_store<D>(j, p, row, lane);
     }
 }
 
@@ -1028,7 +1043,7 @@ __global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ 
                 j.o[0] = fmaf(v.x, w, j.o[0]), j.o[1] = fmaf(v.y, w, j.o[1]);
                 if constexpr (D == 128) j.o[2] = fmaf(v.z, w, j.o[2]), j.o[3] = fmaf(v.w, w, j.o[3]);
             }
-            join_store<D>(j, p0.out, nullptr, row0 + r, lane);
+            join_store<D>(j, p0, row0 + r, lane);
         }
         return;
     }
@@ -1045,7 +1060,7 @@ __global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ 
             if (n == 1) join_add<D>(j, p.whole_o, p.whole_lse, 1, [row](int) { return row; }, lane);
             else join_add<D>(j, p.part_o, p.part_lse, n, PartRow{c, i}, lane);
         }
-        join_store<D>(j, p0.out, nullptr, row, lane);
+        join_store<D>(j, p0, row, lane);
     }
 }
 
@@ -1164,7 +1179,7 @@ FwdLayout fwd_layout_of(const FwdPlan &plan, int64_t d, bool two_sets) {
     return L;
 }
 
-cudaError_t launch_dense_fwd(const DenseProblem &pb, const void *q, const KeySet *sets, int nsets, void *out, float *lse,
+cudaError_t launch_dense_fwd(const DenseProblem &pb, const void *q, const KeySet *sets, int nsets, void *out, void *low, float *lse,
                              float *ws, uint32_t *status, cudaStream_t stream) {
     FwdParams p[2] = {};
     for (int k = 0; k < nsets; ++k) {
@@ -1172,6 +1187,7 @@ cudaError_t launch_dense_fwd(const DenseProblem &pb, const void *q, const KeySet
         x.plan = make_fwd_plan(pb, sets[k]);
         const FwdLayout L = fwd_layout_of(x.plan, pb.d, nsets == 2);
         x.out = static_cast<__nv_bfloat16 *>(out);
+        x.low = static_cast<__nv_bfloat16 *>(low);
         x.lse = lse;
         x.part_o = ws + L.part_o;
         x.part_lse = ws + L.part_lse;

@@ -61,10 +61,6 @@ __device__ __forceinline__ void tmem_wait_ld_of(float (&x)[64]) {
         :
         : "memory");
 }
-__device__ __forceinline__ void tmem_wait_ld_of(float (&x)[128]) {
-    tmem_wait_ld_of(*reinterpret_cast<float (*)[64]>(&x[0]));
-    tmem_wait_ld_of(*reinterpret_cast<float (*)[64]>(&x[64]));
-}
 // Bounded wait (2 s, as wait_bar) that does not read the global timer, which costs more than most waits
 // last, before it has been suspended a few times.
 __device__ __forceinline__ bool wait_soon(uint64_t *b, uint32_t parity, volatile int *abort_flag, uint32_t *status) {
@@ -112,14 +108,16 @@ __device__ __forceinline__ float2 exp2_fma2(float2 x) {
     return __fmul2_rn(p, make_float2(__uint_as_float((__float_as_uint(t.x) << 23) + 0x3f800000u),
                                      __uint_as_float((__float_as_uint(t.y) << 23) + 0x3f800000u)));
 }
-// 32 lanes x 16 columns: thread t of the warp gets TMEM lane (base + t).
-__device__ __forceinline__ void tmem_ld16w(uint32_t taddr, uint32_t *u) {
+// 32 lanes x 16 columns: thread t of the warp gets TMEM lane (base + t), once the load is complete.
+__device__ __forceinline__ void tmem_ld16_now(uint32_t taddr, uint32_t *u) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
         : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
           "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15])
-        : "r"(taddr));
+        : "r"(taddr)
+        : "memory");
 }
 // 32 lanes x 16 columns: thread t of the warp writes TMEM lane (base + t).
 __device__ __forceinline__ void tmem_st16w(uint32_t taddr, const uint32_t *u) {
@@ -152,11 +150,16 @@ __device__ __forceinline__ void store_rows(uint8_t *stage, const uint32_t (&w)[1
     }
     __syncwarp();
 }
-// `cols` accumulator columns (a multiple of 32) of a warp's 32 rows, times f, to global memory: as bf16, or
-// as fp32 parts. dst: lane l's row. zero: the row is zeros whatever the accumulator holds. Not
-// inlined: an epilogue's registers would otherwise spill what the loop around it keeps.
+// What rounding two values to bf16 (w) leaves off, as bf16.
+__device__ __forceinline__ uint32_t rest_bf16x2(float a, float b, uint32_t w) {
+    return pack_bf16x2(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u));
+}
+// `cols` accumulator columns (a multiple of 32) of a warp's 32 rows, times f, to global memory: as bf16 (and
+// what that rounding leaves off to `low`, if it is not null), or as fp32 parts. dst, low: lane l's row.
+// zero: the row is zeros whatever the accumulator holds. Not inlined: an epilogue's registers would
+// otherwise spill what the loop around it keeps.
 static __device__ __noinline__ void write_rows(uint8_t *stage, uint32_t taddr, int cols, float f, bool zero, bool bf16, void *dst,
-                                        bool valid, int lane) {
+                                        void *low, bool valid, int lane) {
 #pragma unroll 1
     for (int cc = 0; cc < cols; cc += 32) {
         float o[32];
@@ -169,6 +172,11 @@ static __device__ __noinline__ void write_rows(uint8_t *stage, uint32_t taddr, i
 #pragma unroll
             for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
             store_rows(stage, w, static_cast<char *>(dst) + 2 * cc, valid, lane);
+            if (__any_sync(0xffffffffu, low != nullptr)) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) w[e] = rest_bf16x2(o[2 * e], o[2 * e + 1], w[e]);
+                store_rows(stage, w, static_cast<char *>(low) + 2 * cc, valid && low, lane);
+            }
         } else {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {

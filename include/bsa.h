@@ -324,6 +324,9 @@ BSA_API bsa_status bsa_forward_noalloc(const bsa_config *cfg, const void *q, con
  *            and flagged BSA_ERR_INDEX in *status_word.
  *   lse      [batch][heads][n_q] ln Σ_j exp(s·q_i·k_j), nullable: what the
  *            backward needs beside out.
+ *   out_low  like out, nullable: what rounding out to bf16 leaves off, as bf16,
+ *            so that out + out_low is good to 17 bits. The backward's row sums
+ *            dout·out are then not spoiled by that rounding.
  * dtype BSA_BF16, head_dim 64 or 128, any n_q, n_k >= 1 (BSA_ERR_UNSUPPORTED
  * for another type or head_dim, or sizes past 32-bit row numbers).
  * Products take bf16 operands (the softmax weights rounded to bf16 for the
@@ -349,12 +352,14 @@ typedef struct {
 
 BSA_API bsa_status bsa_cross_workspace_size(const bsa_cross_config *cfg, size_t *bytes);
 BSA_API bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
-                                       const int32_t *key_len, void *out, float *lse, void *workspace,
-                                       size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream);
+                                       const int32_t *key_len, void *out, float *lse, void *out_low,
+                                       void *workspace, size_t workspace_bytes, uint32_t *status_word,
+                                       cudaStream_t stream);
 
 /*
  * Gradients of the same with respect to q, k and v for dout = dL/dout
- * ([batch][heads][n_q][head_dim], bf16), given out and lse of the forward:
+ * ([batch][heads][n_q][head_dim], bf16), given out, lse and out_low of the
+ * forward (out_low nullable: the row sums then take out's rounding into dq and dk):
  * dq like q, dk and dv like k (the sum over the query heads that share a key
  * head; zero behind key_len). fp32 accumulation, rounded to bf16 once; no
  * atomics, so every gradient is the same bit for bit from call to call.
@@ -363,9 +368,9 @@ BSA_API bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *
 BSA_API bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t *bytes);
 BSA_API bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void *q, const void *k,
                                                 const void *v, const int32_t *key_len, const void *out,
-                                                const float *lse, const void *dout, void *dq, void *dk, void *dv,
-                                                void *workspace, size_t workspace_bytes, uint32_t *status_word,
-                                                cudaStream_t stream);
+                                                const float *lse, const void *out_low, const void *dout, void *dq,
+                                                void *dk, void *dv, void *workspace, size_t workspace_bytes,
+                                                uint32_t *status_word, cudaStream_t stream);
 
 /*
  * Attention of an ensemble whose members share a long prefix of keys (the

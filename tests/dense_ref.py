@@ -6,7 +6,7 @@ error (at most 1e-4 for its polynomial route), and logits summed in 32 bits, an 
 most (d + 2) 2^-24 s sum|q||k| (`logit`). Sums over n terms add n 2^-24.
   out:  a weight rounded to bf16 is off by u, the row sum by EPS, the result is rounded once:
         |err| <= (u + 2 eps) A + u |o|,  A = sum_j p_j |v_j|
-  D = dout.out uses the rounded out: |err D| <= sum_c |dout_c| err_out_c
+  D = dout.out is off by no more than with the rounded out: |err D| <= sum_c |dout_c| err_out_c
   dv:   |err| <= (u + 2 eps) sum_i p_i |dout_i| + u |dv|
   ds = p (dp - D), rounded to bf16: |err ds| <= p ((u + 2 eps) |dp - D| + err D + d 2^-24 sum|dout||v|)
   dq:   |err| <= s sum_j err ds_j |k_j| + (n 2^-24) s sum |ds||k| + u |dq|;  dk the same over rows.

@@ -43,7 +43,7 @@ def test_cross_config_refusals(lib, over, code):
     c = ctypes.byref(cross_cfg(**over))
     assert lib.bsa_cross_workspace_size(c, ctypes.byref(n)) == code
     assert lib.bsa_cross_backward_workspace_size(c, ctypes.byref(n)) == code
-    assert lib.bsa_cross_attention(c, A, 2 * A, 3 * A, None, 4 * A, None, A, 1 << 40, None, None) == code
+    assert lib.bsa_cross_attention(c, A, 2 * A, 3 * A, None, 4 * A, None, None, A, 1 << 40, None, None) == code
 
 
 @pytest.mark.parametrize("over,code", COMMON + [(dict(n_prefix=0), 1), (dict(n_own=0), 1), (dict(groups=0), 1),
@@ -58,26 +58,28 @@ def test_prefix_config_refusals(lib, over, code):
 
 def test_cross_pointer_refusals(lib):
     c = ctypes.byref(cross_cfg())
-    ok = [A, 2 * A, 3 * A, None, 4 * A, None]
+    ok = [A, 2 * A, 3 * A, None, 4 * A, None, None]
     call = lambda a, ws=A, n=1 << 40, st=None: lib.bsa_cross_attention(c, *a, ws, n, st, None)
     for i in (0, 1, 2, 4):                                   # q, k, v, out
         assert call(ok[:i] + [None] + ok[i + 1:]) == 1
         assert call(ok[:i] + [ok[i] + 8] + ok[i + 1:]) == 3
-    assert call(ok[:3] + [A + 2] + ok[4:]) == 3 and call(ok[:5] + [A + 2]) == 3 and call(ok, st=A + 1) == 3
-    assert call(ok[:4] + [A, None]) == 1                     # out is q
+    assert call(ok[:3] + [A + 2] + ok[4:]) == 3 and call(ok[:5] + [A + 2, None]) == 3 and call(ok[:6] + [A + 8]) == 3 and call(ok, st=A + 1) == 3
+    assert call(ok[:4] + [A, None, None]) == 1               # out is q
+    assert call(ok[:6] + [4 * A]) == 1 and call(ok[:6] + [2 * A]) == 1   # out_low is out, k
     assert lib.bsa_cross_workspace_size(c, None) == 1 and lib.bsa_cross_workspace_size(None, None) == 1
 
 
 def test_backward_pointer_refusals(lib):
     c = ctypes.byref(cross_cfg())
-    ok = [A, 2 * A, 3 * A, None, 4 * A, 5 * A, 6 * A, 7 * A, 8 * A, 9 * A]   # q k v len out lse dout dq dk dv
+    ok = [A, 2 * A, 3 * A, None, 4 * A, 5 * A, 10 * A, 6 * A, 7 * A, 8 * A, 9 * A]   # q k v len out lse low dout dq dk dv
     call = lambda a, ws=A, n=1 << 40: lib.bsa_cross_attention_backward(c, *a, ws, n, None, None)
-    for i in (0, 1, 2, 4, 5, 6, 7, 8, 9):
+    for i in (0, 1, 2, 4, 5, 7, 8, 9, 10):
         assert call(ok[:i] + [None] + ok[i + 1:]) == 1
-    for i in (0, 1, 2, 4, 6, 7, 8, 9):
+    for i in (0, 1, 2, 4, 6, 7, 8, 9, 10):
         assert call(ok[:i] + [ok[i] + 8] + ok[i + 1:]) == 3
-    assert call(ok[:7] + [8 * A, 8 * A, 9 * A]) == 1         # dq is dk
-    assert call(ok[:9] + [6 * A]) == 1                       # dv is dout
+    assert call(ok[:8] + [8 * A, 8 * A, 9 * A]) == 1         # dq is dk
+    assert call(ok[:10] + [6 * A]) == 1                      # dv is dout
+    assert call(ok[:10] + [10 * A]) == 1                     # dv is out_low
 
 
 def test_prefix_pointer_refusals(lib):
@@ -94,7 +96,7 @@ def test_workspace_refusals(lib):
     """Sizes whose key axis is split need a workspace, of the stated size and alignment."""
     n = ctypes.c_size_t(0)
     c = ctypes.byref(cross_cfg(batch=1, heads=1, kv_heads=1, n_q=1, n_k=100000))
-    args = [A, 2 * A, 3 * A, None, 4 * A, None]
+    args = [A, 2 * A, 3 * A, None, 4 * A, None, None]
     assert lib.bsa_cross_workspace_size(c, ctypes.byref(n)) == 0
     if n.value:
         assert lib.bsa_cross_attention(c, *args, None, n.value, None, None) == 6

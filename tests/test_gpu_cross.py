@@ -71,12 +71,15 @@ def test_forward_and_gradients(shape):
     ref = dense_ref.cross(q, k, v, lens, dout=g)
     layer = api.CrossAttentionTrain(b, h, nq, nk, d, kv_heads=hk)
     out = layer(q, k, v, lens_of(lens))
-    lse = layer._saved[5]
+    lse, low = layer._saved[5:]
     grads = layer.backward(g)
     plain = api.CrossAttention(b, h, nq, nk, d, kv_heads=hk)(q, k, v, lens_of(lens))
     assert layer.check_status() == 0
     dense_ref.check(out, ref, "out")
     dense_ref.check(lse, ref, "lse")
+    # out + out_low: off by the weights' rounding and 2^-17 of the value, without the result's own rounding
+    ref["both"], ref["both_tol"] = ref["out"], ref["out_tol"] - 1.01 * (dense_ref.U - 2.0 ** -17) * ref["out"].abs()
+    dense_ref.check(out.double() + low.double(), ref, "both")
     for name, x in zip(("dq", "dk", "dv"), grads):
         dense_ref.check(x, ref, name)
     assert torch.equal(plain, out)
