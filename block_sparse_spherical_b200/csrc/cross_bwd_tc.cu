@@ -1,7 +1,7 @@
 // Backward of dense softmax attention to states of another length on the sm_100a
 // tensor cores (bf16, head_dim D = 64 or 128, fp32 accumulation).
 //
-// With the forward's row log-sum-exp and D_i = dout_i·out_i (a row pass ahead):
+// With the forward's row log-sum-exp and D_i = dout_i·(out_i + out_low_i) (a row pass ahead):
 //   s_ij = q_i·k_j,  p_ij = exp(c s_ij - lse_i),  dp_ij = dout_i·v_j,
 //   ds_ij = p_ij (dp_ij - D_i),
 //   dv_j = Σ_i p_ij dout_i,  dk_j = c Σ_i ds_ij q_i,  dq_i = c Σ_j ds_ij k_j.
@@ -20,7 +20,19 @@
 // nothing passes through shared memory. S and dP have barriers of their own, and so have P and
 // dS: exponentials run while dP is formed, P·B1 while dS is computed, and S of the next step
 // as soon as this one's is read (where P has columns of its own) or its P used up (KEY,
-// D = 128, where tensor memory holds no more).
+// D = 128, where tensor memory holds no more; see kParts).
+//
+// Roundings: P and dS are bf16 as operands, as out and the gradients are (each off by half a step, a mean
+// of 1.66e-3 in bf16). For dq, dS is given as two bf16 terms, its rounding and what that leaves off: with one, dq
+// was off by 2.5e-3 of its norm from 64 bits, with two it is 1.7e-3, which is its own rounding. That costs
+// the dq pass a product more (12288 x 12288, 8 heads, D = 64: 652 us, with one term 565). dk
+// and dv (2.4e-3) have no columns of tensor memory left for it. D's own error would be common to
+// a row's dS: from out alone, which is rounded, it took dq and dk to 2.8e-3 at 64 keys.
+//
+// What bounds it: 12288 x 12288, 8 heads, D = 64: dk and dv 718 us, dq 652, the row pass 9, the parts'
+// sum 6; 10 n² d flops a head are 773 GFLOP, 0.56 PFLOP/s of them in 1.39 ms. A step of 128 x 128 needs 1,024
+// clocks of the exponential unit and about as many of the tensor cores; what it takes (2,400) is the chain
+// S, exponentials, P, dP, dS, product, of which only parts overlap in the tensor memory there is.
 //
 // One persistent CTA per SM, 640 threads: warp 0 finds the units, hands them out and copies their tiles,
 // warp 1 issues S and dP, warp 2 P·B1 (KEY), warp 3 dS·B0 (one thread issues a tcgen05 instruction
@@ -30,7 +42,7 @@
 //
 // Tensor memory: S 0..127, dP 128..255. KEY, D = 64: P 256, dS 320 (64 columns each), dv 384, dk 448.
 // KEY, D = 128: P and dS in the place of the thread's own S and dP columns, dv 256, dk 384.
-// !KEY: dS 256, dq 320.
+// !KEY: dS 256, dq 320, dS's second term 448.
 //
 // The steps of all units are dealt to the CTAs in equal shares; a unit cut between CTAs leaves fp32
 // parts, which a last kernel adds in the order of the CTAs.
@@ -143,7 +155,8 @@ template <int D> struct alignas(1024) Shared {
     uint8_t b0[Cfg<D>::STAGES][Cfg<D>::TILE], b1[Cfg<D>::STAGES][Cfg<D>::TILE];
     float stat[Cfg<D>::STAGES][kStat];
     uint64_t u_full[2], u_empty[2], st_full[4], st_empty[4], tail;
-    uint64_t s_full, dp_full, s_free, p_full, ds_full, v_done, k_done, acc_full, acc_free, drain[3];
+    uint64_t s_full[2], dp_full[2], s_free[2], p_full[2], ds_full[2], v_done[2], k_done[2];    // of each part of a step
+    uint64_t acc_full, acc_free, drain[3];
     uint64_t ch_full[kChunks], ch_empty[kChunks];
     Chunk ch[kChunks];
     uint32_t tmem_base;
@@ -322,11 +335,19 @@ __device__ void copy_role(const BwdParams &p, const BwdMaps &maps, Shared<D> &sh
 constexpr uint32_t kColS = 0, kColDp = 128;
 // P and dS take the place of S and dP
 template <int D, bool KEY> constexpr bool kInPlace = KEY && D == 128;
+// Then a step's columns are handed over in two halves with barriers of their own: one half's softmax runs
+// beside the products that the other's columns have to wait for (three entries of 4004 rows and up to 2345
+// keys, dk and dv: 70 us, in one piece 76.5). Elsewhere S and dP of the next step are formed ahead, and
+// twice as many products of half the width cost more than the halves gain (12288 x 12288, 8 heads,
+// D = 64: 735 us, in one piece 718).
+template <int D, bool KEY> constexpr int kParts = kInPlace<D, KEY> ? 2 : 1;
+template <int D, bool KEY> constexpr int kWide = kTile / kParts<D, KEY>;    // columns of a part
 // P and dS of columns 32w..32w+31 of a step
 template <int D, bool KEY> __device__ __forceinline__ uint32_t col_p(int w) { return kInPlace<D, KEY> ? 32u * w : 256u + 16u * w; }
 template <int D, bool KEY> __device__ __forceinline__ uint32_t col_ds(int w) {
     return kInPlace<D, KEY> ? 128u + 32u * w : (KEY ? 320u : 256u) + 16u * w;
 }
+constexpr uint32_t kDsLow = 192;            // !KEY: from a column of dS to that of what its rounding leaves off
 template <int D, bool KEY> constexpr uint32_t kColV = D == 64 ? 384u : 256u;
 template <int D, bool KEY> constexpr uint32_t kColK = !KEY ? 320u : (D == 64 ? 448u : 384u);
 
@@ -341,11 +362,13 @@ __device__ void score_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int
     };
     const uint64_t a0 = desc_kmajor_sw128(sh.a0[0]), a1 = desc_kmajor_sw128(sh.a1[0]);
     const uint64_t b0 = desc_kmajor_sw128(sh.b0[0]), b1 = desc_kmajor_sw128(sh.b1[0]);
-    auto product = [&](uint32_t col, uint64_t a, uint64_t b) __attribute__((always_inline)) {
+    constexpr int PARTS = kParts<D, KEY>, WIDE = kWide<D, KEY>;
+    // part h of a step's columns
+    auto product = [&](uint32_t col, uint64_t a, uint64_t b, int h) __attribute__((always_inline)) {
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
             const uint64_t off = (kk / 4) * ((kTile * 128) >> 4) + 2 * (kk % 4);
-            mma_bf16(tmem + col, a + off, b + off, idesc_of(kTile, false), kk > 0);
+            mma_bf16(tmem + col + WIDE * h, a + off, b + off + h * ((WIDE * 128) >> 4), idesc_of(WIDE, false), kk > 0);
         }
     };
     uint32_t u = 0, g = 0;
@@ -361,24 +384,31 @@ __device__ void score_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int
         for (int t = 0; t < nt; ++t, ++g) {
             const int st = g % C::STAGES;
             if (!(ok = wait_w(&sh.st_full[st], (g / C::STAGES) & 1))) break;
-            // the columns of S are free: read by the softmax, or (P in their place) by P·B1
-            if (g > 0 && !(ok = wait_w(kInPlace<D, KEY> ? &sh.v_done : &sh.s_free, (g - 1) & 1))) break;
-            fence_after();
-            if (leader) {
-                product(kColS, a0 + (uint64_t)(ub * (C::TILE >> 4)), b0 + (uint64_t)(st * (C::TILE >> 4)));
-                commit(&sh.s_full);
+            for (int h = 0; h < PARTS; ++h) {
+                // the columns of S are free: read by the softmax, or (P in their place) by P·B1
+                if (g > 0 && !(ok = wait_w(kInPlace<D, KEY> ? &sh.v_done[h] : &sh.s_free[h], (g - 1) & 1))) break;
+                fence_after();
+                if (leader) {
+                    product(kColS, a0 + (uint64_t)(ub * (C::TILE >> 4)), b0 + (uint64_t)(st * (C::TILE >> 4)), h);
+                    commit(&sh.s_full[h]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
-            // those of dP: read, as dS of the step before is written, or (dS in their place) used up
-            if (g > 0 && !(ok = wait_w(kInPlace<D, KEY> ? &sh.k_done : &sh.ds_full, (g - 1) & 1))) break;
-            fence_after();
-            if (leader) {
-                product(kColDp, a1 + (uint64_t)(ub * (C::TILE >> 4)), b1 + (uint64_t)(st * (C::TILE >> 4)));
-                commit(&sh.dp_full);
-                commit(&sh.st_empty[st]);
-                if (t + 1 == nt) commit(&sh.u_empty[ub]);
+            for (int h = 0; h < PARTS && ok; ++h) {
+                // those of dP: read, as dS of the step before is written, or (dS in their place) used up
+                if (g > 0 && !(ok = wait_w(kInPlace<D, KEY> ? &sh.k_done[h] : &sh.ds_full[h], (g - 1) & 1))) break;
+                fence_after();
+                if (leader) {
+                    product(kColDp, a1 + (uint64_t)(ub * (C::TILE >> 4)), b1 + (uint64_t)(st * (C::TILE >> 4)), h);
+                    commit(&sh.dp_full[h]);
+                    if (h == PARTS - 1) {
+                        commit(&sh.st_empty[st]);
+                        if (t + 1 == nt) commit(&sh.u_empty[ub]);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
         }
     }
     // every MMA this warp issued must be complete before TMEM is freed
@@ -391,6 +421,7 @@ __device__ void score_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int
 template <int D, bool KEY, bool V>
 __device__ void grad_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int lane) {
     using C = Cfg<D>;
+    constexpr int PARTS = kParts<D, KEY>, WIDE = kWide<D, KEY>;
     constexpr uint32_t A_STEP = kInPlace<D, KEY> ? 32 : 16;    // columns of P and dS from w to w + 1
     volatile int *abort_flag = &sh.abort_flag;
     const bool leader = elect_one();
@@ -410,30 +441,35 @@ __device__ void grad_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int 
         ++u;
         for (int t = 0; t < nt; ++t, ++g) {
             const int st = g % C::STAGES;
-            if (!(ok = wait_w(V ? &sh.p_full : &sh.ds_full, g & 1))) break;
-            fence_after();
-            if (leader) {
-                const uint64_t b = b0 + (uint64_t)(st * (C::TILE >> 4));
+            for (int h = 0; h < PARTS; ++h) {
+                if (!(ok = wait_w(V ? &sh.p_full[h] : &sh.ds_full[h], g & 1))) break;
+                fence_after();
+                if (leader) {
+                    const uint64_t b = b0 + (uint64_t)(st * (C::TILE >> 4)) + 8 * WIDE * h;
+                    const uint32_t a = from + WIDE / 32 * A_STEP * h;
 #pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)        // blocks of 16 columns of the step
-                    mma_ts(acc, from + A_STEP * (kk >> 1) + 8u * (kk & 1), b + 128 * kk, idesc_of(D, true), t > 0 || kk > 0);
-                commit(V ? &sh.v_done : &sh.k_done);
-                commit(&sh.st_empty[st]);
-                if (t + 1 == nt) commit(&sh.acc_full);
+                    for (int kk = 0; kk < WIDE / 16; ++kk)    // blocks of 16 columns of the step
+                        mma_ts(acc, a + A_STEP * (kk >> 1) + 8u * (kk & 1), b + 128 * kk, idesc_of(D, true), t > 0 || h > 0 || kk > 0);
+                    if constexpr (!KEY) {
+#pragma unroll
+                        for (int kk = 0; kk < WIDE / 16; ++kk)
+                            mma_ts(acc, a + kDsLow + 8u * kk, b + 128 * kk, idesc_of(D, true), 1u);
+                    }
+                    commit(V ? &sh.v_done[h] : &sh.k_done[h]);
+                    if (h == PARTS - 1) {
+                        commit(&sh.st_empty[st]);
+                        if (t + 1 == nt) commit(&sh.acc_full);
+                    }
+                }
+                __syncwarp();
             }
-            __syncwarp();
+            if (!ok) break;
         }
     }
     if (leader) commit(&sh.drain[V ? 1 : 2]);
     __syncwarp();
     drain_bar(&sh.drain[V ? 1 : 2], 0);
 }
-
-// Of 16 pairs of exponentials, how many take the polynomial on the FMA pipe.
-#ifndef KPOLYB
-#define KPOLYB 0
-#endif
-constexpr int kPoly = KPOLYB;
 
 template <int D, bool KEY>
 __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, int w, int wq, int lane) {
@@ -445,6 +481,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
     };
     const uint32_t tw = tmem + ((uint32_t)(32 * wq) << 16);
     const int row = 32 * wq + lane;          // this thread's row of the unit
+    const int part = w / (kWide<D, KEY> / 32);   // its part of a step
     const float2 sl2 = make_float2(p.scale_log2, p.scale_log2);
     uint32_t u = 0, g = 0;
     bool ok = true;
@@ -460,7 +497,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
         }
         for (int t = 0; t < nt; ++t, ++g) {
             const int st = g % C::STAGES;
-            if (!(ok = wait_all(&sh.s_full, g & 1))) break;
+            if (!(ok = wait_all(&sh.s_full[part], g & 1))) break;
             // KEY: the statistics arrived with the step's tiles; this thread's own wait on their barrier (long
             // complete) makes the copied values visible to it
             if (KEY && !(ok = wait_all(&sh.st_full[st], (g / C::STAGES) & 1))) break;
@@ -470,7 +507,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
             tmem_wait_ld_of(x);
             if constexpr (!IN_PLACE) {
                 fence_before();
-                warp_arrive(&sh.s_free, lane);
+                warp_arrive(&sh.s_free[part], lane);
             }
             // p = 2^(c·log2 e·s - lse·log2 e), in place, 16 at a time
             const float4 *ls4 = reinterpret_cast<const float4 *>(sh.stat[st] + 32 * w);
@@ -487,7 +524,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 }
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    e2[e] = (8 * h + e) * kPoly % 16 < kPoly ? exp2_fma2(e2[e]) : make_float2(ex2(e2[e].x), ex2(e2[e].y));
+                    e2[e] = make_float2(ex2(e2[e].x), ex2(e2[e].y));
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     x[16 * h + 2 * e] = e2[e].x;
@@ -502,7 +539,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
             }
             // the columns that P and dS take are free: the gradients' products of the step before have read them
             // (in place: before this S and this dP began)
-            if (KEY && !IN_PLACE && g > 0 && !(ok = wait_all(&sh.v_done, (g - 1) & 1))) break;
+            if (KEY && !IN_PLACE && g > 0 && !(ok = wait_all(&sh.v_done[part], (g - 1) & 1))) break;
             if constexpr (KEY) {
                 fence_after();
                 uint32_t pk[16];
@@ -511,12 +548,12 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 tmem_st16w(tw + col_p<D, KEY>(w), pk);
                 tmem_wait_st();
                 fence_before();
-                warp_arrive(&sh.p_full, lane);
+                warp_arrive(&sh.p_full[part], lane);
             }
-            if (!(ok = wait_all(&sh.dp_full, g & 1))) break;
+            if (!(ok = wait_all(&sh.dp_full[part], g & 1))) break;
             fence_after();
             float d[32];
-            uint32_t ds[16];
+            uint32_t ds[16], low[16];
             tmem_ld32(tw + kColDp + 32u * w, d);
             tmem_wait_ld_of(d);
 #pragma unroll
@@ -529,21 +566,27 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
                                             __fadd2_rn(make_float2(d[c + 2], d[c + 3]), make_float2(d4.z, d4.w)));
                 ds[2 * e] = pack_bf16x2(a.x, a.y);
                 ds[2 * e + 1] = pack_bf16x2(b.x, b.y);
+                if (!KEY) {
+                    low[2 * e] = rest_bf16x2(a.x, a.y, ds[2 * e]);
+                    low[2 * e + 1] = rest_bf16x2(b.x, b.y, ds[2 * e + 1]);
+                }
             }
             // what does not count is 0 whatever dP holds there (0·NaN)
             if (KEY ? !counts : valid < 32) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
-                    if (KEY || 2 * e >= valid) ds[e] = 0u;
-                    else if (2 * e + 1 >= valid) ds[e] &= 0xffffu;
+                    const uint32_t keep = KEY || 2 * e >= valid ? 0u : (2 * e + 1 >= valid ? 0xffffu : 0xffffffffu);
+                    ds[e] &= keep;
+                    if (!KEY) low[e] &= keep;
                 }
             }
-            if (!IN_PLACE && g > 0 && !(ok = wait_all(&sh.k_done, (g - 1) & 1))) break;
+            if (!IN_PLACE && g > 0 && !(ok = wait_all(&sh.k_done[part], (g - 1) & 1))) break;
             fence_after();
             tmem_st16w(tw + col_ds<D, KEY>(w), ds);
+            if (!KEY) tmem_st16w(tw + col_ds<D, KEY>(w) + kDsLow, low);
             tmem_wait_st();
             fence_before();
-            warp_arrive(&sh.ds_full, lane);
+            warp_arrive(&sh.ds_full[part], lane);
         }
         if (!ok) break;
         if (nt > 0) {
@@ -553,13 +596,13 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
         }
         // KEY: w = 0, 1 store dv's columns, 2, 3 dk's (nothing where no key counts); !KEY: dq's, D / 4 each
         // (D = 64: w = 0, 1)
-        const int grad = KEY ? w >> 1 : 1, part = KEY ? w & 1 : w, wide = KEY ? D / 2 : 32;
+        const int grad = KEY ? w >> 1 : 1, piece = KEY ? w & 1 : w, wide = KEY ? D / 2 : 32;
         const uint32_t col = grad == 0 ? kColV<D, KEY> : kColK<D, KEY>;
         const int64_t at = cp->slab * (KEY ? p.plan.s.n : p.plan.rows) + (int64_t)cp->tile * kTile + row;
         const int slot = cp->slot;
         __nv_bfloat16 *d16 = (!KEY ? p.dq : grad == 0 ? p.dv : p.dk) + at * D;
         float *d32 = p.part + ((2 * (int64_t)blockIdx.x + max(slot, 0)) * kTile + row) * (KEY ? 2 * D : D) + (KEY ? grad * D : 0);
-        const int c0 = part * wide;
+        const int c0 = piece * wide;
         if (nt > 0 && c0 < D) {
             // staged in the unit's own tiles, which no product reads any more
             const int ub = (u + C::UB - 1) % C::UB;
@@ -601,13 +644,16 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant_
             mbar_init(&sh.ch_empty[i], kReaders<KEY>);
         }
         mbar_init(&sh.tail, 1);
-        mbar_init(&sh.s_full, 1);
-        mbar_init(&sh.dp_full, 1);
-        mbar_init(&sh.s_free, kSoftWarps);
-        mbar_init(&sh.p_full, kSoftWarps);
-        mbar_init(&sh.ds_full, kSoftWarps);
-        mbar_init(&sh.v_done, 1);
-        mbar_init(&sh.k_done, 1);
+        constexpr int WARPS = kSoftWarps / kParts<D, KEY>;      // softmax warps of a part
+        for (int h = 0; h < kParts<D, KEY>; ++h) {
+            mbar_init(&sh.s_full[h], 1);
+            mbar_init(&sh.dp_full[h], 1);
+            mbar_init(&sh.s_free[h], WARPS);
+            mbar_init(&sh.p_full[h], WARPS);
+            mbar_init(&sh.ds_full[h], WARPS);
+            mbar_init(&sh.v_done[h], 1);
+            mbar_init(&sh.k_done[h], 1);
+        }
         mbar_init(&sh.acc_full, KEY ? 2 : 1);
         mbar_init(&sh.acc_free, kSoftWarps);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");

@@ -152,7 +152,9 @@ __device__ __forceinline__ void store_rows(uint8_t *stage, const uint32_t (&w)[1
 }
 // What rounding two values to bf16 (w) leaves off, as bf16.
 __device__ __forceinline__ uint32_t rest_bf16x2(float a, float b, uint32_t w) {
-    return pack_bf16x2(a - __uint_as_float(w << 16), b - __uint_as_float(w & 0xffff0000u));
+    const float2 r = __ffma2_rn(make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)),
+                                make_float2(-1.f, -1.f), make_float2(a, b));
+    return pack_bf16x2(r.x, r.y);
 }
 // `cols` accumulator columns (a multiple of 32) of a warp's 32 rows, times f, to global memory: as bf16 (and
 // what that rounding leaves off to `low`, if it is not null), or as fp32 parts. dst, low: lane l's row.
