@@ -342,7 +342,7 @@ class CrossAttentionTrain(CrossAttention):
         lse = torch.empty(self.shape[:3], dtype=torch.float32, device=self.device)
         low = torch.empty(self.shape, dtype=self.dtype, device=self.device)
         out = self._forward(q, k, v, key_len, out, lse, low)
-        self._saved = (q, k, v, key_len, out, lse, low)
+        self._saved, self._stream = (q, k, v, key_len, out, lse, low), torch.cuda.current_stream(self.device)
         return out
 
     def backward(self, dout, grads=None):
@@ -350,6 +350,10 @@ class CrossAttentionTrain(CrossAttention):
         if self._saved is None:
             raise RuntimeError("backward() needs a forward() first")
         saved = self._saved
+        stream = torch.cuda.current_stream(self.device)
+        if stream != self._stream:          # a later forward() must not hand these out before they are read
+            for t in saved[-2:]:
+                t.record_stream(stream)
         outs = [self._output(t, name, shape, like) for t, name, shape, like in
                 zip(grads or (None,) * 3, ("dq", "dk", "dv"), (self.shape, self.kv_shape, self.kv_shape), saved)]
         args = (*(None if t is None else t.data_ptr() for t in saved), self._take(dout, "dout", self.shape),

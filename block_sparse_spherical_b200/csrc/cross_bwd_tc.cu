@@ -7,8 +7,8 @@
 //   dv_j = Σ_i p_ij dout_i,  dk_j = c Σ_i ds_ij q_i,  dq_i = c Σ_j ds_ij k_j.
 // Two passes of one kernel, each with its sums in tensor memory, so that no gradient is
 // reduced through atomics and all are the same from call to call; the second recomputes
-// s and dp (7 products a pair of tiles where one pass would need 5 and an fp32
-// reduction of dq through L2 in an order that changes).
+// s and dp (8 products a pair of tiles, two of them dq's, where one pass would need 5 and
+// an fp32 reduction of dq through L2 in an order that changes).
 //
 // A unit is a tile of 128 rows of one side, with operands A0 and A1, a step a tile of 128 of
 // the other, with B0 and B1:

@@ -6,25 +6,26 @@
 //   s_ij = q_i·k_j (·s log2 e),  m_i = max_j s_ij (lazily: it may lag by up to 2^8),
 //   p_ij = 2^(s_ij - m_i),  l_i = Σ_j p_ij,  o_i = Σ_j p_ij v_j / l_i.
 // A step is one tile of 128 keys: S = Q·Kᵀ (tcgen05.mma, M = N = 128) into tensor
-// memory, softmax numerators by 128 threads (a thread owns a row), P as bf16 pairs
-// back into tensor memory, O += P·V with P as the A operand from there.
+// memory, softmax numerators by the threads of its rows, P as bf16 pairs back into
+// tensor memory, O += P·V with P as the A operand from there.
 //
-// Organisation: one persistent CTA per SM, 384 threads, two pipelines:
+// Organisation: one persistent CTA per SM, two pipelines:
 //   warp 0       copies (TMA, 128-byte swizzle): Q of a unit, then K and V tiles
 //                through one ring that both pipelines read
 //   warps 1, 2   the MMA warp of pipeline 0 and of pipeline 1
 //   warp 3       finds the CTA's units and hands them out
-//   warps 4-7, 8-11  softmax and epilogue of pipeline 0 and of pipeline 1
+//   warps 4..    softmax and epilogue of pipeline 0, then of pipeline 1: four warps
+//                each, or eight (many rows, D = 64)
 // Many rows: the pipelines hold two tiles of 128 rows of one unit and both take
-// every key tile, so K and V are read once for 256 rows. A thread owns a row.
-//   D = 64: a step is a key tile. S of the next one is formed as soon as this one's is read, and
-//   P has columns of its own; a thread keeps P in registers until the P·V before it has read
-//   those (waiting for that ahead of the exponentials put P·V's whole chain, from the arrival of P to
-//   its completion about 1,000 clocks, into every step: 2.09 us for 256 rows and 128 keys, where the
-//   exponentials alone need 1.08).
-//   D = 128: tensor memory has no columns left for that. A step is half a key tile, S has two buffers,
-//   P(u) takes the place of S(u): the MMA warp issues S(0) S(1) PV(0) S(2) PV(1) ..., so that the
-//   products of one step run beside the softmax of the other.
+// every key tile, so K and V are read once for 256 rows.
+//   D = 64 (640 threads, two for a row, each with half of a tile's keys): a step is a key tile. S of the next
+//   one is formed as soon as this one's is read, and P has columns of its own; a thread keeps P in
+//   registers until the P·V before it has read those (waiting for that ahead of the exponentials put
+//   P·V's whole chain, from the arrival of P to its completion about 1,000 clocks, into every step:
+//   2.09 us for 256 rows and 128 keys, where the exponentials alone need 1.08).
+//   D = 128 (384 threads, one for a row): tensor memory has no columns left for that. A step is half a key
+//   tile, S has two buffers, P(u) takes the place of S(u): the MMA warp issues S(0) S(1) PV(0)
+//   S(2) PV(1) ..., so that the products of one step run beside the softmax of the other.
 // Few rows (at most 32: a decoding step's query heads, or an ensemble's members
 // together): both pipelines hold the same rows, four times over in the four 32-lane
 // quarters of tensor memory, and take alternate key tiles; warp w of a pipeline does
@@ -38,6 +39,16 @@
 //
 // Keys behind a length: scores are replaced before the maximum (whatever K holds),
 // and the copy warp zeroes those rows of V in shared memory, since 0·NaN is NaN.
+//
+// Roundings: the weights are bf16 as an operand (V's type; their sums are taken before that, in fp32), out
+// is bf16: each half a step, together 2.3e-3 of out's norm from 64 bits, where rounding out alone gives
+// 1.7e-3. out_low carries what rounding out leaves off to the backward's row sums.
+//
+// What bounds it and what it takes: 12288 rows a head, 8 heads, on 29040 keys, D = 64: 915 us, 0.80 PFLOP/s; the
+// exponential unit alone needs 634 us of that (16 a clock and SM), a step of 256 rows and 128 keys takes
+// 1.55 us, the rest being the chain S, maximum, exponentials, P, P·V of each pipeline where the
+// other does not cover it. 12288 on 12288: 443 us. Few rows: 24 entries of one row, 16 heads on
+// 4 key heads, D = 128, 29040 keys: 211 us, the keys' and values' 1.43 GB at the rate of memory, 6.8 TB/s.
 //
 // Every wait on an mbarrier is bounded (2 s), as in the block-sparse kernel.
 #include <math_constants.h>
@@ -65,8 +76,9 @@ template <int D, bool FEW> struct Threads {
 };
 constexpr int kSub = 64;                    // keys of a step when there are many rows
 // Of 16 pairs of exponentials, how many take the polynomial on the FMA pipe. D = 64 is bound by the
-// exponentials (a step of 256 rows and 128 keys: none 1.86 us, 4 of 16 1.69, 6 of 16 1.75), D = 128
-// by the chain of its products (none 2.33 us, 4 of 16 2.44).
+// exponentials and what goes out beside them (12288 x 29040, 8 heads: none 980 us, 1 of 16 974, 2 of 16
+// 922, 4 of 16 940), D = 128 by the chain of its products (a step of 256 rows and 128 keys: none 2.33 us,
+// 4 of 16 2.44).
 template <int D> constexpr int kPoly = D == 64 ? 2 : 0;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -827,7 +839,8 @@ __global__ void __launch_bounds__((Threads<D, FEW>::ALL), 1) dense_fwd_kernel(co
                                                                 const __grid_constant__ FwdParams p) {
     fwd_cta<D, FEW, Threads<D, FEW>>(maps, p);
 }
-// Two sets in one launch, the first set's CTAs first: the second's begin on each SM as the first's end there.
+// Two sets in one launch, the first set's CTAs first: the second's begin on each SM as the first's end there
+// (four members of 3 rows on 777 shared and 77 own keys: 15 us, in two launches 23).
 template <int D, bool FEW0, bool FEW1>
 __global__ void __launch_bounds__((Threads<D, FEW0>::ALL), 1)
 dense_fwd_pair_kernel(const __grid_constant__ Maps maps0, const __grid_constant__ FwdParams p0, const __grid_constant__ Maps maps1,
@@ -1111,8 +1124,9 @@ template <int D> cudaError_t run(const DenseProblem &pb, const void *q, const Ke
     // the rows of a set are those of its members together: at least as many in the first set
     const bool few0 = p[0].plan.s.few, few1 = p[1].plan.s.few;
     if (few0 && !few1) return cudaErrorInvalidValue;
-    // Short passes share the SMs by their steps (and one for each unit's end); of long ones the second follows
-    // the first on each SM, which needs no guess of what a step of either costs.
+    // Short passes share the SMs by their steps (and one for each unit's end: 24 members' rows on 12288 shared
+    // and 40 own keys, D = 128: 27 us, one after the other 31); of long ones the second follows the first on
+    // each SM, which needs no guess of what a step of either costs.
     int64_t work[2];
     for (int k = 0; k < 2; ++k) {
         const FwdSet &s = p[k].plan.s;
