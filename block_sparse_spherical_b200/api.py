@@ -162,7 +162,7 @@ class BSATrain(BSA):
         self.lse_fine = torch.empty((b, h, n, 2), dtype=torch.float32, device=dev)
         self.bwd_workspace_bytes = abi.bsa_backward_workspace_size(self.cfg)
         self.bwd_workspace = torch.zeros(self.bwd_workspace_bytes, dtype=torch.uint8, device=dev)
-        self._saved = None
+        self._saved = self._stream = None
 
     def __call__(self, q, k, v, gates, out=None) -> torch.Tensor:
         return self.forward(q, k, v, gates, out)
@@ -340,9 +340,9 @@ class CrossAttentionTrain(CrossAttention):
 
     def forward(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
         lse = torch.empty(self.shape[:3], dtype=torch.float32, device=self.device)
-        low = torch.empty(self.shape, dtype=self.dtype, device=self.device)
+        low = torch.empty_like(q)
         out = self._forward(q, k, v, key_len, out, lse, low)
-        self._saved, self._stream = (q, k, v, key_len, out, lse, low), torch.cuda.current_stream(self.device)
+        self._saved, self._stream = (q, k, v, key_len, out, lse, low), _raw_stream(self.device.index)
         return out
 
     def backward(self, dout, grads=None):
@@ -350,10 +350,9 @@ class CrossAttentionTrain(CrossAttention):
         if self._saved is None:
             raise RuntimeError("backward() needs a forward() first")
         saved = self._saved
-        stream = torch.cuda.current_stream(self.device)
-        if stream != self._stream:          # a later forward() must not hand these out before they are read
-            for t in saved[-2:]:
-                t.record_stream(stream)
+        if _raw_stream(self.device.index) != self._stream:
+            for t in saved[4:]:             # a later forward() must not hand these out before they are read
+                t.record_stream(torch.cuda.current_stream(self.device))
         outs = [self._output(t, name, shape, like) for t, name, shape, like in
                 zip(grads or (None,) * 3, ("dq", "dk", "dv"), (self.shape, self.kv_shape, self.kv_shape), saved)]
         args = (*(None if t is None else t.data_ptr() for t in saved), self._take(dout, "dout", self.shape),

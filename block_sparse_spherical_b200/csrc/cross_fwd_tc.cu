@@ -44,10 +44,10 @@
 // is bf16: each half a step, together 2.3e-3 of out's norm from 64 bits, where rounding out alone gives
 // 1.7e-3. out_low carries what rounding out leaves off to the backward's row sums.
 //
-// What bounds it and what it takes: 12288 rows a head, 8 heads, on 29040 keys, D = 64: 915 us, 0.80 PFLOP/s; the
+// What bounds it and what it takes: 12288 rows a head, 8 heads, on 29040 keys, D = 64: 920 us, 0.79 PFLOP/s; the
 // exponential unit alone needs 634 us of that (16 a clock and SM), a step of 256 rows and 128 keys takes
 // 1.55 us, the rest being the chain S, maximum, exponentials, P, P·V of each pipeline where the
-// other does not cover it. 12288 on 12288: 443 us. Few rows: 24 entries of one row, 16 heads on
+// other does not cover it. 12288 on 12288: 450 us. Few rows: 24 entries of one row, 16 heads on
 // 4 key heads, D = 128, 29040 keys: 211 us, the keys' and values' 1.43 GB at the rate of memory, 6.8 TB/s.
 //
 // Every wait on an mbarrier is bounded (2 s), as in the block-sparse kernel.
@@ -97,6 +97,8 @@ struct Chunk {
     int nt, t0, rel;        // rel: the set's keys from key tile t0 on
     int slot;               // -1: the whole unit
     int alone;              // many rows: the second pipeline has no tile
+    int rows[2];            // tiles of one member's rows: how many, from row row0 on
+    int64_t row0[2];
     int64_t z, hk, pair;
 };
 struct Walk {
@@ -205,6 +207,14 @@ __device__ __forceinline__ bool walk_next(const FwdParams &p, Walk &w, Chunk &c,
     c.nt = min(steps, tiles - c.t0);                   // 0 for a set without keys
     c.rel = len - c.t0 * kTile;
     c.alone = 2 * c.pair + 1 >= s.tiles;
+    if (!s.bb) {
+#pragma unroll
+        for (int pl = 0; pl < 2; ++pl) {
+            const int64_t t = 2 * c.pair + pl, member = quotient(t, s.tpm), r = (t - member * s.tpm) * kTile;
+            c.rows[pl] = t < s.tiles ? (int)min((int64_t)kTile, p.plan.rows - r) : 0;
+            c.row0[pl] = ((c.z * s.members + member) * p.plan.kv_heads + c.hk) * p.plan.rows + r;
+        }
+    }
     return true;
 }
 
@@ -482,7 +492,7 @@ __device__ __forceinline__ void numerators(const float *s, float sl2, float neg_
     }
 }
 
-// Where row i (of the unit's 256) of a chunk goes: out and lse, a part, or a whole row of a set.
+// Where row i of tile pl of a chunk's unit goes: out and lse, a part, or a whole row of a set.
 struct RowOut {
     __nv_bfloat16 *o16, *low;
     float *o32, *lse;
@@ -490,9 +500,9 @@ struct RowOut {
     bool valid, bf16;       // bf16: o16, for all rows of the chunk
 };
 template <int D>
-__device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, int64_t tile, int i_tile, int i_unit) {
+__device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, int pl, int i) {
     RowOut r;
-    const int64_t row = plan_row(p.plan, c.z, c.hk, tile, i_tile);
+    const int64_t row = p.plan.s.bb ? plan_row(p.plan, c.z, c.hk, 2 * c.pair + pl, i) : i < c.rows[pl] ? c.row0[pl] + i : -1;
     r.valid = row >= 0;
     r.o16 = r.low = nullptr;
     r.o32 = r.lse = nullptr;
@@ -500,7 +510,7 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
     r.bf16 = c.slot < 0 && !p.whole_o;
     if (!r.valid) return r;
     if (c.slot >= 0) {
-        const int64_t at = (2 * (int64_t)this_cta(p) + c.slot) * (2 * kTile) + i_unit;
+        const int64_t at = (2 * (int64_t)this_cta(p) + c.slot) * (2 * kTile) + kTile * pl + i;
         r.o32 = p.part_o + at * D;
         r.lse = p.part_lse + at;
     } else if (p.whole_o) {
@@ -514,6 +524,38 @@ __device__ __forceinline__ RowOut row_out(const FwdParams &p, const Chunk &c, in
         r.lse_unit = kLn2;
     }
     return r;
+}
+
+// A warp's rows j0..j1-1 (lane j knows row j's places) of a set without keys: zeros and lse = -inf (of a set among two
+// lse alone is read). Many such units may follow one another on a CTA, each counted as one step: with
+// the stores of other units they held up a forward (4 x 4004 rows of an empty entry among three) to 70 us, so 49.
+template <int D> __device__ __forceinline__ void zero_rows(const RowOut &r, int j0, int j1, int lane) {
+    constexpr int LANES = D / 8;                       // of a row
+    auto fill = [&](__nv_bfloat16 *mine) {
+#pragma unroll 2
+        for (int j = j0; j < j1; j += 32 / LANES) {
+            char *to = reinterpret_cast<char *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), j + lane / LANES));
+            if (to) *reinterpret_cast<uint4 *>(to + 16 * (lane % LANES)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    fill(r.o16);
+    fill(r.low);
+    if (j0 == 0 && r.valid && r.lse) *r.lse = -CUDART_INF_F;
+}
+// The end of a unit of many rows: a warp's 32 rows, columns [c0, c0 + COLS) of o at taddr, and lse (with c0 = 0).
+template <int D, int COLS>
+__device__ __forceinline__ void end_rows(const FwdParams &p, const Chunk &c, int pl, int wq, int c0, uint32_t taddr, float m, float l,
+                                      uint8_t *stage, int lane) {
+    const RowOut r = row_out<D>(p, c, pl, 32 * wq + lane);
+    if (c.nt <= 0) {                                   // a set without keys: half of the rows each
+        zero_rows<D>(r, 32 * c0 / D, 32 * (c0 + COLS) / D, lane);
+        return;
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    write_rows(stage, taddr, COLS, inv, l == 0.f, r.bf16, r.bf16 ? static_cast<void *>(r.o16 + c0) : r.o32 + c0,
+               r.low ? r.low + c0 : nullptr, r.valid, lane);
+    if (c0 == 0 && r.valid && r.lse) *r.lse = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * r.lse_unit;
 }
 
 template <int D, bool FEW>
@@ -644,13 +686,8 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                 ++nl;
                 l = ls[0] + ls[kTile];
             }
-            const RowOut r = row_out<D>(p, *cp, 2 * cp->pair + pl, 32 * wq + lane, kTile * pl + 32 * wq + lane);
-            const float inv = l == 0.f ? 0.f : 1.f / l;
             uint8_t *stage = reinterpret_cast<uint8_t *>(sh.merge) + 2048 * (4 * (SPLIT * pl + hh) + wq);
-            void *dst = r.bf16 ? static_cast<void *>(r.o16 + COLS * hh) : r.o32 + COLS * hh;
-            write_rows(stage, tO + COLS * hh, COLS, inv, n == 0 || l == 0.f, r.bf16, dst,
-                       r.low ? r.low + COLS * hh : nullptr, r.valid, lane);
-            if (hh == 0 && r.valid && r.lse) *r.lse = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * r.lse_unit;
+            end_rows<D, COLS>(p, *cp, pl, wq, COLS * hh, tO + COLS * hh, m, l, stage, lane);
             fence_before();
             chunk_done<D>(sh, i, lane);
         } else {
@@ -740,7 +777,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                         y.z += z.z;
                         y.w += z.w;
                     }
-                    const RowOut r = row_out<D>(p, *cp, 0, r0 + mr, r0 + mr);
+                    const RowOut r = row_out<D>(p, *cp, 0, r0 + mr);
                     if (r.valid) {
                         if (r.o16) {
                             const uint2 u = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
@@ -760,7 +797,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
         }
         if (!ok) break;
         if (idx == 0 && lane < nrows) {
-            const RowOut r = row_out<D>(p, *cp, 0, lane, lane);
+            const RowOut r = row_out<D>(p, *cp, 0, lane);
             if (r.valid && r.lse) *r.lse = L == 0.f ? -CUDART_INF_F : (M + __log2f(L)) * r.lse_unit;
         }
         fence_before();

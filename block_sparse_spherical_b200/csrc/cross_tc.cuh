@@ -168,7 +168,14 @@ static __device__ __noinline__ void write_rows(uint8_t *stage, uint32_t taddr, i
         tmem_ld32(taddr + cc, o);
         tmem_wait_ld_of(o);
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = zero ? 0.f : o[e] * f;
+        for (int e = 0; e < 32; e += 2) {
+            const float2 y = __fmul2_rn(make_float2(o[e], o[e + 1]), make_float2(f, f));
+            o[e] = y.x, o[e + 1] = y.y;
+        }
+        if (__any_sync(0xffffffffu, zero)) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = zero ? 0.f : o[e];
+        }
         uint32_t w[16];
         if (bf16) {
 #pragma unroll

@@ -6,16 +6,19 @@ error (at most 1e-4 for its polynomial route), and logits summed in 32 bits, an 
 most (d + 2) 2^-24 s sum|q||k| (`logit`). Sums over n terms add n 2^-24.
   out:  a weight rounded to bf16 is off by u, the row sum by EPS, the result is rounded once:
         |err| <= (u + 2 eps) A + u |o|,  A = sum_j p_j |v_j|
-  D = dout.out is off by no more than with the rounded out: |err D| <= sum_c |dout_c| err_out_c
+  D = dout.(out + out_low), where out_low is what rounding out leaves off, itself rounded (2^-17 of out):
+        |err D| <= sum_c |dout_c| ((u + 2 eps) A_c + 2^-17 |o_c|)
   dv:   |err| <= (u + 2 eps) sum_i p_i |dout_i| + u |dv|
   ds = p (dp - D), rounded to bf16: |err ds| <= p ((u + 2 eps) |dp - D| + err D + d 2^-24 sum|dout||v|)
-  dq:   |err| <= s sum_j err ds_j |k_j| + (n 2^-24) s sum |ds||k| + u |dq|;  dk the same over rows.
+  dk:   |err| <= s sum_i err ds_i |q_i| + (rows 2^-24) s sum |ds||q| + u |dk|
+  dq:   the same over keys, with ds in two bf16 terms: 2^-17 in place of its u.
 """
 import math
 
 import torch
 
 U = 2.0 ** -8
+TWO = 2.0 ** -17        # of two bf16 terms: half a step of 8 bits below the first one's half step
 F = 2.0 ** -24
 EXP = 1e-4
 
@@ -46,12 +49,13 @@ def attend(q, k, v, scale, dout=None):
     dterm = (g * o).sum(-1, keepdim=True)
     ds = p * (dp - dterm)
     e = eps + (rows * F)
-    w = p * ((U + 2 * e) * (dp - dterm).abs() + (g.abs() * out_tol).sum(-1, keepdim=True)
-             + d * F * (g.abs() @ v.abs().T))
+    both_tol = 1.01 * ((U + 2 * eps) * (p @ v.abs()) + TWO * o.abs())
+    w, w2 = (p * ((u + 2 * e) * (dp - dterm).abs() + (g.abs() * both_tol).sum(-1, keepdim=True)
+                  + d * F * (g.abs() @ v.abs().T)) for u in (U, TWO))
     r["dv"] = p.T @ g
     r["dv_tol"] = 1.01 * (((U + 2 * e) * p).T @ g.abs() + U * r["dv"].abs())
     r["dq"], r["dk"] = scale * (ds @ k), scale * (ds.T @ q)
-    r["dq_tol"] = 1.01 * (scale * (w @ k.abs() + n * F * (ds.abs() @ k.abs())) + U * r["dq"].abs())
+    r["dq_tol"] = 1.01 * (scale * (w2 @ k.abs() + n * F * (ds.abs() @ k.abs())) + U * r["dq"].abs())
     r["dk_tol"] = 1.01 * (scale * (w.T @ q.abs() + rows * F * (ds.abs().T @ q.abs())) + U * r["dk"].abs())
     return r
 

@@ -152,11 +152,13 @@ def test_bounds_hold_for_a_simulated_kernel_and_catch_mistakes():
     m = s.amax(-1, keepdim=True)
     w = torch.exp(s - m)
     z = w.sum(-1, keepdim=True)
-    out = bf(bf(w) @ vf / z)
+    exact = bf(w) @ vf / z
+    out = bf(exact)
     p = w / z
-    dterm = (gf * out).sum(-1, keepdim=True)
-    ds = bf(p * (gf @ vf.T - dterm))
-    got = dict(out=out, dv=bf(bf(p).T @ gf), dq=bf(ds @ kf / 8), dk=bf(ds.T @ qf / 8))
+    dterm = (gf * (out + bf(exact - out))).sum(-1, keepdim=True)
+    full = p * (gf @ vf.T - dterm)
+    ds = bf(full)
+    got = dict(out=out, dv=bf(bf(p).T @ gf), dq=bf((ds + bf(full - ds)) @ kf / 8), dk=bf(ds.T @ qf / 8))
     for name, x in got.items():
         dense_ref.check(x[None, None], ref, name)
     wrong = dict(out=bf(bf(w[:, 1:]) @ vf[1:] / z), dq=bf(ds @ kf), dk=bf(bf(p * (gf @ vf.T)).T @ qf / 8))

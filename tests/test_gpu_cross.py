@@ -78,13 +78,67 @@ def test_forward_and_gradients(shape):
     dense_ref.check(out, ref, "out")
     dense_ref.check(lse, ref, "lse")
     # out + out_low: off by the weights' rounding and 2^-17 of the value, without the result's own rounding
-    ref["both"], ref["both_tol"] = ref["out"], ref["out_tol"] - 1.01 * (dense_ref.U - 2.0 ** -17) * ref["out"].abs()
+    ref["both"], ref["both_tol"] = ref["out"], ref["out_tol"] - 1.01 * (dense_ref.U - dense_ref.TWO) * ref["out"].abs()
     dense_ref.check(out.double() + low.double(), ref, "both")
     for name, x in zip(("dq", "dk", "dv"), grads):
         dense_ref.check(x, ref, name)
     assert torch.equal(plain, out)
     again = layer.backward(g)
     assert all(torch.equal(x, y) for x, y in zip(grads, again)), "gradients change from call to call"
+
+
+# more units than SMs, so that a CTA takes several, whole and cut; few rows and many; more entries with lengths
+# than are added up to cut units
+LONG = [
+    (40, 8, 8, 2, 700, 64, [0, 1, 128, 129, 700] * 8),
+    (40, 8, 8, 3, 260, 128, None),
+    (30, 8, 4, 9, 2600, 128, None),
+    (30, 8, 4, 9, 2600, 64, list(range(0, 2600, 87))),
+    (4, 8, 8, 1100, 200, 128, [200, 0, 1, 130]),
+    (5, 8, 8, 1030, 130, 64, None),
+    (2, 8, 8, 2500, 520, 64, [520, 77]),
+    (2, 8, 4, 1250, 520, 128, [520, 385]),
+    (1, 16, 4, 8, 30000, 64, None),
+    (1100, 1, 1, 2, 140, 64, [i % 141 for i in range(1100)]),
+    (1100, 2, 1, 70, 129, 128, [(7 * i) % 130 for i in range(1100)]),
+]
+
+
+@pytest.mark.parametrize("shape", LONG, ids=lambda s: "-".join(map(str, s[:6])))
+def test_many_units(shape):
+    test_forward_and_gradients(shape)
+
+
+def test_offsets_past_32_bits():
+    """Keys and values of 2.3e9 elements (the last slab holds what is compared), then rows of as many."""
+    b, hk, n, d = 17, 8, 132000, 128
+    gen = torch.Generator(device="cuda").manual_seed(20)
+    k, v = (torch.empty((b, hk, n, d), dtype=BF, device="cuda") for _ in range(2))
+    assert k.numel() > 2 ** 31
+    for t in (k, v):
+        t[:] = normal(gen, n, d)
+        t[-1, -1] = normal(gen, n, d)
+    q = normal(gen, b, hk, 1, d, size=2.0)
+    out = api.CrossAttention(b, hk, 1, n, d)(q, k, v)
+    for i, e in ((0, 0), (b - 1, hk - 1)):
+        ref = dense_ref.attend(q[i, e], k[i, e], v[i, e], d ** -0.5)
+        dense_ref.check(out[i, e], ref, "out", f"slab {i}, {e}")
+    del k, v, out
+    rows, n, d = 2 ** 25 + 300, 130, 64
+    q, g = (torch.empty((1, 1, rows, d), dtype=BF, device="cuda") for _ in range(2))
+    assert q.numel() > 2 ** 31
+    q[:], g[:] = normal(gen, d), 0.0
+    last = slice(rows - 1000, rows)
+    q[0, 0, last], g[0, 0, last] = normal(gen, 1000, d, size=2.0), normal(gen, 1000, d)
+    k, v = normal(gen, 1, 1, n, d), normal(gen, 1, 1, n, d)
+    layer = api.CrossAttentionTrain(1, 1, rows, n, d)
+    out = layer(q, k, v)
+    dq, dk, dv = layer.backward(g)
+    ref = dense_ref.attend(q[0, 0, last], k[0, 0], v[0, 0], d ** -0.5, g[0, 0, last])     # the others have no gradient
+    dense_ref.check(out[0, 0, last], ref, "out")
+    for name, x in (("dq", dq[0, 0, last]), ("dk", dk[0, 0]), ("dv", dv[0, 0])):
+        dense_ref.check(x, ref, name)
+    assert not dq[0, 0, :rows - 1000].any() and layer.check_status() == 0
 
 
 @pytest.mark.parametrize("d", [64, 128])
@@ -159,6 +213,11 @@ PREFIX = [
     (2, 70, 2, 1, 1, 1000, 9, 64, None, None),
     (1, 5, 3, 1, 11, 128, 128, 64, [0], [0, 1, 0, 128, 100]),
     (2, 2, 1, 1, 300, 640, 200, 64, None, [200, 0]),
+    (1, 8, 8, 8, 300, 2000, 300, 64, None, None),
+    (2, 8, 8, 8, 300, 1500, 400, 128, [1500, 1], [400, 0, 399, 128, 129, 1, 5, 77]),
+    (1, 60, 8, 4, 3, 6000, 50, 64, None, None),
+    (5, 200, 4, 2, 3, 700, 30, 128, [700, 0, 128, 1, 300], None),
+    (1, 2, 8, 8, 1, 30000, 3, 128, None, [3, 0]),
 ]
 
 
@@ -201,6 +260,62 @@ def test_another_stream_and_two_at_once():
                 o.append(layer(*a))
     torch.cuda.synchronize()
     assert all(torch.equal(x, w) for o, w in zip(got, want) for x in o)
+
+
+def test_prefix_on_two_streams_and_in_graphs():
+    """One layer's calls that overlap, eager ones and two graphs' of the same capture-time buffers."""
+    gen = torch.Generator(device="cuda").manual_seed(18)
+    g, b, h, hk, nq, npre, nown, d = 2, 12, 4, 2, 9, 3000, 200, 64
+    layer = api.PrefixAttention(b, h, nq, npre, nown, d, kv_heads=hk, groups=g)
+    shapes = ((b, h, nq, d), (g, hk, npre, d), (g, hk, npre, d), (b, hk, nown, d), (b, hk, nown, d))
+    args = [normal(gen, *s) for s in shapes]
+    own = lens_of([(37 * i) % 201 for i in range(b)])
+    call = lambda: layer(*args, own_len=own)
+    call()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            outs.append(call())
+        graphs.append(gr)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    for _ in range(3):
+        for x in args:
+            x.copy_(normal(gen, *x.shape))
+        own.copy_(own.roll(1))
+        want = call()
+        torch.cuda.synchronize()
+        for gr, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                gr.replay()
+        with torch.cuda.stream(streams[2]):
+            got = call()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, want) for x in (*outs, got))
+    dense_ref.check(got, dense_ref.prefix(*args, None, own.tolist()), "out")
+    assert layer.check_status() == 0
+
+
+def test_backward_on_another_stream_than_the_forward():
+    """What the layer keeps for the backward outlives a forward that replaces it while that backward waits."""
+    q, k, v, g = inputs(1, 4, 2, 400, 3000, 64, seed=19)
+    layer = api.CrossAttentionTrain(1, 4, 400, 3000, 64, kv_heads=2)
+    layer(q, k, v)
+    want = layer.backward(g)
+    side = torch.cuda.Stream()
+    for _ in range(5):
+        layer(q, k, v)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                layer.backward(g)
+            got = layer.backward(g)
+        junk = api.CrossAttentionTrain(1, 4, 400, 3000, 64, kv_heads=2)
+        layer(v[:, :, :400].repeat(1, 2, 1, 1), k, v)                # replaces what was kept
+        junk(v[:, :, :400].repeat(1, 2, 1, 1), k, v)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
 def test_captured_graphs_replay_with_new_inputs():
