@@ -76,9 +76,11 @@ struct BwdParams {
     __nv_bfloat16 *dq, *dk, *dv;
     float *part;            // KEY [2 ctas][128][2][D] (dv, dk), !KEY [2 ctas][128][D]
     Cut *cuts;              // [ctas], stream only
+    int cta0;               // first block of this pass in the launch
     float scale, scale_log2;
     uint32_t *status;
 };
+__device__ __forceinline__ int this_cta(const BwdParams &p) { return (int)blockIdx.x - p.cta0; }
 struct BwdMaps {
     CUtensorMap a0, a1, b0, b1;
 };
@@ -173,10 +175,10 @@ template <bool KEY> __device__ __forceinline__ int64_t units_of(const FwdPlan &p
 __device__ __forceinline__ Walk walk_begin(const BwdParams &p, int lane) {
     Walk w{};
     if (p.plan.stream) {
-        if (lane == 0) p.cuts[blockIdx.x].last = -1;   // until one is noted
+        if (lane == 0) p.cuts[this_cta(p)].last = -1;  // until one is noted
         w.total = total_steps(p.plan, lane);
-        w.at = cta_first(blockIdx.x, w.total, p.plan.ctas);
-        w.left = cta_first(blockIdx.x + 1, w.total, p.plan.ctas) - w.at;
+        w.at = cta_first(this_cta(p), w.total, p.plan.ctas);
+        w.left = cta_first(this_cta(p) + 1, w.total, p.plan.ctas) - w.at;
         if (w.left > 0) {
             const StepAt at = step_at(p.plan, w.at, lane);
             w.t = at.t;
@@ -185,7 +187,7 @@ __device__ __forceinline__ Walk walk_begin(const BwdParams &p, int lane) {
             w.uu = at.uu;
         }
     } else {
-        w.left = blockIdx.x;
+        w.left = this_cta(p);
     }
     return w;
 }
@@ -225,12 +227,12 @@ template <bool KEY> __device__ __forceinline__ bool walk_next(const BwdParams &p
     c.slab = z * hk_n + hk;
     if (p.plan.stream) {
         if (lead && w.t == 0 && c.slot == 1)
-            p.cuts[blockIdx.x] = Cut{(int)z, (int)hk, c.tile, cta_of(w.at + w.steps - 1, w.total, p.plan.ctas)};
+            p.cuts[this_cta(p)] = Cut{(int)z, (int)hk, c.tile, cta_of(w.at + w.steps - 1, w.total, p.plan.ctas)};
         w.t += n;
         w.at += n;
         w.left -= n;
     } else {
-        w.left += gridDim.x;
+        w.left += p.plan.ctas;
     }
     if (KEY) {
         c.rows = len - c.tile * kTile;
@@ -601,7 +603,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
         const int64_t at = cp->slab * (KEY ? p.plan.s.n : p.plan.rows) + (int64_t)cp->tile * kTile + row;
         const int slot = cp->slot;
         __nv_bfloat16 *d16 = (!KEY ? p.dq : grad == 0 ? p.dv : p.dk) + at * D;
-        float *d32 = p.part + ((2 * (int64_t)blockIdx.x + max(slot, 0)) * kTile + row) * (KEY ? 2 * D : D) + (KEY ? grad * D : 0);
+        float *d32 = p.part + ((2 * (int64_t)this_cta(p) + max(slot, 0)) * kTile + row) * (KEY ? 2 * D : D) + (KEY ? grad * D : 0);
         const int c0 = piece * wide;
         if (nt > 0 && c0 < D) {
             // staged in the unit's own tiles, which no product reads any more
@@ -623,8 +625,7 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
     }
 }
 
-template <int D, bool KEY>
-__global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant__ BwdMaps maps, const __grid_constant__ BwdParams p) {
+template <int D, bool KEY> __device__ __forceinline__ void bwd_cta(const BwdMaps &maps, const BwdParams &p) {
     extern __shared__ uint8_t smem_raw[];
     Shared<D> &sh = *reinterpret_cast<Shared<D> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     const int warp = uniform((int)threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -690,6 +691,15 @@ __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant_
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+}
+
+// Both passes in one launch, dk's and dv's CTAs first: few units of either run beside one another, and of
+// many the dq pass begins on each SM as the other ends there.
+template <int D>
+__global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant__ BwdMaps maps_key, const __grid_constant__ BwdParams key,
+                                                          const __grid_constant__ BwdMaps maps_qry, const __grid_constant__ BwdParams qry) {
+    if ((int)blockIdx.x < qry.cta0) bwd_cta<D, true>(maps_key, key);
+    else bwd_cta<D, false>(maps_qry, qry);
 }
 
 // ---------------------------------------------------------------- parts added
@@ -807,16 +817,13 @@ cudaError_t launch(const DenseProblem &pb, const void *q, const KeySet &ks, cons
     mq.b1 = mk.a1;
     const size_t smem = sizeof(Shared<D>) + 1024;
     static_assert(sizeof(Shared<D>) + 1024 <= 232448, "shared memory");
-    cudaError_t e = kernel_ready<bwd_kernel<D, true>>(smem, NTHREADS, kRegsNeeded);
-    if (e == cudaSuccess) e = kernel_ready<bwd_kernel<D, false>>(smem, NTHREADS, kRegsNeeded);
+    cudaError_t e = kernel_ready<bwd_kernel<D>>(smem, NTHREADS, kRegsNeeded);
     if (e != cudaSuccess) return e;
     const int64_t rows_a_block = 256 / (D / 8), stat_blocks = (slabs * plans.qtiles * kTile + rows_a_block - 1) / rows_a_block;
     bwd_stat_kernel<D><<<(unsigned)(stat_blocks < 8 * kCtas ? stat_blocks : 8 * kCtas), 256, 0, stream>>>(
         key, static_cast<const __nv_bfloat16 *>(out), static_cast<const __nv_bfloat16 *>(low), lse, static_cast<const __nv_bfloat16 *>(dout), stat, slabs);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    bwd_kernel<D, true><<<key.plan.ctas, NTHREADS, smem, stream>>>(mk, key);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    bwd_kernel<D, false><<<qry.plan.ctas, NTHREADS, smem, stream>>>(mq, qry);
+    bwd_kernel<D><<<key.plan.ctas + qry.plan.ctas, NTHREADS, smem, stream>>>(mk, key, mq, qry);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     constexpr int PER = kTile / (8 * kJoinRows);
     const int kb = key.cuts ? key.plan.ctas * PER : 0, qb = qry.cuts ? qry.plan.ctas * PER : 0;
@@ -846,6 +853,7 @@ cudaError_t launch_dense_bwd(const DenseProblem &pb, const void *q, const KeySet
     key.status = status;
     BwdParams qry = key;
     qry.plan = plans.qry;
+    qry.cta0 = plans.key.ctas;
     qry.part = ws + plans.qry_part;
     qry.cuts = plans.qry.stream ? reinterpret_cast<Cut *>(ws + plans.qry_cuts) : nullptr;
     float *stat = ws + plans.stat;
