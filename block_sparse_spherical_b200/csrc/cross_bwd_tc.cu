@@ -29,8 +29,8 @@
 // and dv (2.4e-3) have no columns of tensor memory left for it. D's own error would be common to
 // a row's dS: from out alone, which is rounded, it took dq and dk to 2.8e-3 at 64 keys.
 //
-// What bounds it: 12288 x 12288, 8 heads, D = 64: dk and dv 718 us, dq 652, the row pass 9, the parts'
-// sum 6; 10 n² d flops a head are 773 GFLOP, 0.56 PFLOP/s of them in 1.39 ms. A step of 128 x 128 needs 1,024
+// What bounds it: 12288 x 12288, 8 heads, D = 64: both passes 1,365 us (alone: dk and dv 718, dq 650),
+// the row pass 9, the parts' sum 6; 10 n² d flops a head are 773 GFLOP, 0.56 PFLOP/s of them in 1.39 ms. A step of 128 x 128 needs 1,024
 // clocks of the exponential unit and about as many of the tensor cores; what it takes (2,400) is the chain
 // S, exponentials, P, dP, dS, product, of which only parts overlap in the tensor memory there is.
 //
@@ -694,7 +694,8 @@ template <int D, bool KEY> __device__ __forceinline__ void bwd_cta(const BwdMaps
 }
 
 // Both passes in one launch, dk's and dv's CTAs first: few units of either run beside one another, and of
-// many the dq pass begins on each SM as the other ends there.
+// many the dq pass begins on each SM as the other ends there (768 rows, 200 keys, 2 heads, D = 64: 14 us, in two
+// launches 23).
 template <int D>
 __global__ void __launch_bounds__(NTHREADS, 1) bwd_kernel(const __grid_constant__ BwdMaps maps_key, const __grid_constant__ BwdParams key,
                                                           const __grid_constant__ BwdMaps maps_qry, const __grid_constant__ BwdParams qry) {

@@ -405,13 +405,12 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
                     if (leader) mbar_arrive(&sh.q_empty[pl]);
                     __syncwarp();
                 } else {
-                    constexpr bool ahead = D == 64 && C::STAGES >= 6;
                     if (!(ok = there(pos + 2 * first))) break;
                     issue_s(g, pos + 2 * first, 0, true, alone, first + by >= nt);
                     for (int t = first; t < nt && ok; t += by) {
                         const bool more = t + by < nt;
                         const uint32_t kn = pos + 2 * (t + by), v = pos + 2 * t + 1;
-                        if (ahead) {                   // P has columns of its own: S as soon as the last one is read
+                        if constexpr (D == 64) {       // P has columns of its own: S as soon as the last one is read
                             if (more) {
                                 if (!(ok = there(kn) && wait_w(&sh.s_free[pl], g & 1))) break;
                                 issue_s(g + 1, kn, 0, true, alone, t + 2 * by >= nt);
@@ -1020,17 +1019,19 @@ template <int D> __global__ void __launch_bounds__(256) join_cut_kernel(const __
     }
 }
 
-// Two sets: a warp joins two rows' parts of both. Where no unit is cut into more than four, all their loads
-// go out together.
-constexpr int kSetRows = 2;
-template <int D>
-__global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ FwdParams p0, const __grid_constant__ FwdParams p1) {
+// Two sets: a warp joins its ROWS rows' parts of both. Where no unit is cut into more than four, all their loads
+// go out together; else one row follows the other. So a warp has one row while one wave of blocks holds them
+// (384 rows of 37 + 1 parts, D = 128: 7.1 us, two rows a warp 10.9), two where there are more (49152
+// rows, D = 64: 19.0 us, one row a warp 24.1). Four blocks an SM need 64 registers a thread, which
+// two rows of D = 128 do not fit.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256, D == 64 || ROWS == 1 ? 4 : 2) join_sets_kernel(const __grid_constant__ FwdParams p0, const __grid_constant__ FwdParams p1) {
     using V = typename std::conditional<D == 64, float2, float4>::type;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t row0 = ((int64_t)blockIdx.x * 8 + warp) * kSetRows;
+    const int64_t row0 = ((int64_t)blockIdx.x * 8 + warp) * ROWS;
     // lane 2r + k: where row r's parts of set k are: parts from CTA ca on at row i of a unit, or one whole row
     int count = 0, ca = 0, at = 0;
-    if (lane < 2 * kSetRows && row0 + (lane >> 1) < p0.all_rows) {
+    if (lane < 2 * ROWS && row0 + (lane >> 1) < p0.all_rows) {
         const FwdParams &p = lane & 1 ? p1 : p0;
         const FwdSet &s = p.plan.s;
         const int64_t row = row0 + (lane >> 1);
@@ -1057,10 +1058,10 @@ __global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ 
     }
     const int most = __reduce_max_sync(0xffffffffu, count);
     if (most <= kJoinParts) {
-        V y[kSetRows][2][kJoinParts];
-        float ls[kSetRows][2][kJoinParts];
+        V y[ROWS][2][kJoinParts];
+        float ls[ROWS][2][kJoinParts];
 #pragma unroll
-        for (int r = 0; r < kSetRows; ++r)
+        for (int r = 0; r < ROWS; ++r)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const FwdParams &p = k ? p1 : p0;
@@ -1077,7 +1078,7 @@ __global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ 
                 }
             }
 #pragma unroll
-        for (int r = 0; r < kSetRows; ++r) {
+        for (int r = 0; r < ROWS; ++r) {
             if (row0 + r >= p0.all_rows) continue;
             Joined<D> j;
             join_begin<D>(j);
@@ -1097,7 +1098,7 @@ __global__ void __launch_bounds__(256) join_sets_kernel(const __grid_constant__ 
         }
         return;
     }
-    for (int r = 0; r < kSetRows; ++r) {
+    for (int r = 0; r < ROWS; ++r) {
         const int64_t row = row0 + r;
         if (row >= p0.all_rows) return;
         Joined<D> j;
@@ -1178,8 +1179,10 @@ template <int D> cudaError_t run(const DenseProblem &pb, const void *q, const Ke
         : few1 ? launch_pair<D, false, true>(maps, p, stream)
                : launch_pair<D, false, false>(maps, p, stream);
     if (e != cudaSuccess) return e;
-    constexpr int rows = 8 * kSetRows;
-    join_sets_kernel<D><<<(unsigned)((p[0].all_rows + rows - 1) / rows), 256, 0, stream>>>(p[0], p[1]);
+    if (p[0].all_rows <= 8 * 4 * kCtas)
+        join_sets_kernel<D, 1><<<(unsigned)((p[0].all_rows + 7) / 8), 256, 0, stream>>>(p[0], p[1]);
+    else
+        join_sets_kernel<D, 2><<<(unsigned)((p[0].all_rows + 15) / 16), 256, 0, stream>>>(p[0], p[1]);
     return cudaGetLastError();
 }
 
