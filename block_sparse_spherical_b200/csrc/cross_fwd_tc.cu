@@ -351,12 +351,19 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
         return __all_sync(0xffffffffu, wait_soon(b, par, abort_flag, p.status));
     };
     auto there = [&](uint32_t at) -> bool { return wait_w(&sh.kv_full[at % C::STAGES], (at / C::STAGES) & 1); };
-    auto release = [&](int st, bool alone) {           // by the leader; alone: for the other pipeline too
-        commit(&sh.kv_empty[st]);
-        if (alone) commit(&sh.kv_empty[st]);
+    // A tile that only the other pipeline uses. Its arrival is waited for and its stages are given back all the
+    // same: a pipeline that let a stage's turn pass could take the one before for the one it waits for (a
+    // barrier tells two turns apart, not three), and did where a tile came in late.
+    auto skip = [&](int t) -> bool {
+        for (uint32_t at = pos + 2 * t; at < pos + 2 * t + 2; ++at) {
+            if (!there(at)) return false;
+            if (leader) mbar_arrive(&sh.kv_empty[at % C::STAGES]);
+            __syncwarp();
+        }
+        return true;
     };
     // S(gs) = Q·Kᵀ of KEYS keys from key `from` of the tile at ring position `at`, which is there
-    auto issue_s = [&](uint32_t gs, uint32_t at, int from, bool done, bool alone, bool last) {
+    auto issue_s = [&](uint32_t gs, uint32_t at, int from, bool done, bool last) {
         const int st = at % C::STAGES, b = gs & 1;
         fence_after();
         if (leader) {
@@ -367,13 +374,13 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
                 mma_bf16(tS + (WHOLE ? 0u : 64u * b), dq + off, dk + off, idesc_of(KEYS, false), kk > 0);
             }
             commit(&sh.s_full[pl][b]);
-            if (done) release(st, alone);
+            if (done) commit(&sh.kv_empty[st]);
             if (last) commit(&sh.q_empty[pl]);
         }
         __syncwarp();
     };
     // O += P·V of step g once P is written; the tile at `at` is there
-    auto issue_pv = [&](uint32_t at, int from, bool done, bool alone, bool first) -> bool {
+    auto issue_pv = [&](uint32_t at, int from, bool done, bool first) -> bool {
         const int st = at % C::STAGES, b = g & 1;
         if (!wait_w(&sh.p_full[pl][b], (g >> 1) & 1)) return false;
         fence_after();
@@ -383,7 +390,7 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
             for (int kk = 0; kk < KEYS / 16; ++kk)
                 mma_ts(tO, tP + (WHOLE ? 0u : 64u * b) + 8u * kk, dv + 128 * kk, idesc_of(D, true), (first && kk == 0) ? 0u : 1u);
             commit(&sh.o_done[pl][b]);
-            if (done) release(st, alone);
+            if (done) commit(&sh.kv_empty[st]);
         }
         __syncwarp();
         ++g;
@@ -393,32 +400,36 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
     for (uint32_t i = 0; ok && (cp = chunk_at<D>(p, sh, i, ok)); ++i) {
         // uniform over the warp, for the compiler too: the MMAs' descriptors then need no vector registers
         const int nt = uniform(cp->nt), rel = uniform(cp->rel);
-        const bool alone = FEW || uniform(cp->alone);  // no other pipeline takes these tiles
+        const bool idle = !FEW && pl == 1 && uniform(cp->alone);   // no tile of rows here
         chunk_done<D>(sh, i, lane);
-        if (nt > 0 && (FEW || pl == 0 || !alone)) {
+        if (idle) {
+            for (int t = 0; t < nt && ok; ++t) ok = skip(t);
+        } else if (nt > 0) {
             if (!(ok = wait_w(&sh.q_full[pl], nq & 1))) break;
             ++nq;
             if constexpr (WHOLE) {
                 constexpr int by = FEW ? 2 : 1;        // few rows: every other tile
                 const int first = FEW ? pl : 0;
+                if (FEW && first > 0 && !(ok = skip(0))) break;
                 if (first >= nt) {                     // one tile: this pipeline's Q stays unused
                     if (leader) mbar_arrive(&sh.q_empty[pl]);
                     __syncwarp();
                 } else {
                     if (!(ok = there(pos + 2 * first))) break;
-                    issue_s(g, pos + 2 * first, 0, true, alone, first + by >= nt);
+                    issue_s(g, pos + 2 * first, 0, true, first + by >= nt);
                     for (int t = first; t < nt && ok; t += by) {
                         const bool more = t + by < nt;
                         const uint32_t kn = pos + 2 * (t + by), v = pos + 2 * t + 1;
+                        if (FEW && D == 64 && t + 1 < nt && !(ok = skip(t + 1))) break;
                         if constexpr (D == 64) {       // P has columns of its own: S as soon as the last one is read
                             if (more) {
                                 if (!(ok = there(kn) && wait_w(&sh.s_free[pl], g & 1))) break;
-                                issue_s(g + 1, kn, 0, true, alone, t + 2 * by >= nt);
+                                issue_s(g + 1, kn, 0, true, t + 2 * by >= nt);
                             }
-                            ok = there(v) && issue_pv(v, 0, true, alone, t == first);
+                            ok = there(v) && issue_pv(v, 0, true, t == first);
                         } else {
-                            ok = there(v) && issue_pv(v, 0, true, alone, t == first) && (!more || there(kn));
-                            if (ok && more) issue_s(g, kn, 0, true, alone, t + 2 * by >= nt);
+                            ok = there(v) && issue_pv(v, 0, true, t == first) && (t + 1 >= nt || skip(t + 1)) && (!more || there(kn));
+                            if (ok && more) issue_s(g, kn, 0, true, t + 2 * by >= nt);
                         }
                     }
                 }
@@ -427,14 +438,14 @@ __device__ void mma_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int p
                 if (!(ok = there(pos))) break;
                 const uint32_t g0 = g;
                 auto s_step = [&](int u) {
-                    issue_s(g0 + u, pos + 2 * (u >> 1), kSub * (u & 1), (u & 1) || u + 1 == n, alone, u + 1 == n);
+                    issue_s(g0 + u, pos + 2 * (u >> 1), kSub * (u & 1), (u & 1) || u + 1 == n, u + 1 == n);
                 };
                 s_step(0);
                 if (n > 1) s_step(1);
                 for (int u = 0; u < n && ok; ++u) {
                     const uint32_t v = pos + 2 * (u >> 1) + 1;
                     ok = ((u & 1) || there(v)) && (u + 2 >= n || (u & 1) || there(pos + u + 2)) &&
-                         issue_pv(v, kSub * (u & 1), (u & 1) || u + 1 == n, alone, u == 0);
+                         issue_pv(v, kSub * (u & 1), (u & 1) || u + 1 == n, u == 0);
                     if (ok && u + 2 < n) s_step(u + 2);
                 }
             }
