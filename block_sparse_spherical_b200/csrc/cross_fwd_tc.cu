@@ -921,7 +921,10 @@ __device__ __forceinline__ void join_add(Joined<D> &j, const float *o, const flo
         float mx = mine;
         for (int i = 16; i; i >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, i));
         const float mn = fmaxf(j.m, mx);
-        if (mn == -CUDART_INF_F) continue;             // no keys in any part so far
+        if (mn == -CUDART_INF_F) {                     // no keys in any part so far, or NaN, which a maximum passes over
+            if (__any_sync(0xffffffffu, mine != mine)) j.l = CUDART_NAN_F;
+            continue;
+        }
         const float a = ex2(j.m - mn), wt = ex2(mine - mn);
         float sum = wt;
         for (int i = 16; i; i >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, i);

@@ -1,0 +1,70 @@
+"""Dense attention at its edges on the GPU: NaN and infinities in rows that count, key axes that are cut,
+calls that meet on several streams and graphs (needs a B200)."""
+import pytest
+import torch
+
+import dense_ref
+from block_sparse_spherical_b200 import abi, api
+from test_gpu_cross import inputs, lens_of, normal
+
+pytestmark = pytest.mark.gpu
+BF = torch.bfloat16
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _cuda():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    abi.load()
+
+
+# n_q, n_k, key_len: whole units; few rows cut into two parts, into more than four, into more than 32; many rows cut
+# into two or three parts and into more than four; a cut unit beside an empty entry
+CUT = [(1, 700, None), (1, 1300, None), (3, 9000, None), (32, 30000, None), (200, 3000, None), (200, 30000, None),
+       (1, 20000, [20000, 0])]
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", CUT, ids=str)
+def test_a_query_row_that_is_not_finite_gives_nan(shape, d, bad):
+    """Scores of a NaN query are NaN, those of an infinite one infinite of both signs: out, lse and dq are NaN in that
+    row, dk and dv in every state it meets, however many parts its keys are cut into. Other rows stay."""
+    nq, nk, lens = shape
+    b = len(lens) if lens else 1
+    q, k, v, g = inputs(b, 2, 2, nq, nk, d, seed=31)
+    row = nq // 2
+    q[0, 1, row, 5] = bad
+    layer = api.CrossAttentionTrain(b, 2, nq, nk, d)
+    out = layer(q, k, v, lens_of(lens))
+    lse = layer._saved[5]
+    dq, dk, dv = layer.backward(g)
+    assert layer.check_status() == 0
+    for x in (out, lse, dq):
+        assert torch.isnan(x[0, 1, row]).all()
+    assert torch.isnan(dk[0, 1]).all() and torch.isnan(dv[0, 1]).all()
+    keep = [i for i in range(nq) if i != row]
+    for x in (out, lse, dq):
+        assert torch.isfinite(x[0, 0]).all() and torch.isfinite(x[0, 1, keep]).all()
+    assert torch.isfinite(dk[0, 0]).all() and torch.isfinite(dv[0, 0]).all()
+    if lens:
+        assert not out[1].any() and not dq[1].any() and not dk[1].any() and (lse[1] == -INF).all()
+
+
+@pytest.mark.parametrize("bad", [NAN, INF])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", [(2, 1, 300, 20), (4, 3, 20000, 77), (4, 150, 30000, 300), (2, 1, 30000, 20000)],
+                         ids=str)
+def test_a_query_row_that_is_not_finite_gives_nan_over_a_prefix(shape, d, bad):
+    b, nq, npre, nown = shape
+    gen = torch.Generator(device="cuda").manual_seed(32)
+    q = normal(gen, b, 2, nq, d, size=2.0)
+    kp, vp, ko, vo = (normal(gen, *s) for s in ((1, 2, npre, d), (1, 2, npre, d), (b, 2, nown, d), (b, 2, nown, d)))
+    q[1, 1, nq // 2, 3] = bad
+    layer = api.PrefixAttention(b, 2, nq, npre, nown, d)
+    for plen, olen in ((None, None), ([npre], [0] * b), ([0], [nown] * b)):
+        out = layer(q, kp, vp, ko, vo, lens_of(plen), lens_of(olen))
+        assert torch.isnan(out[1, 1, nq // 2]).all()
+        out[1, 1, nq // 2] = 0
+        assert torch.isfinite(out).all() and layer.check_status() == 0
