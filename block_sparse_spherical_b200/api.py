@@ -351,8 +351,11 @@ class CrossAttentionTrain(CrossAttention):
             raise RuntimeError("backward() needs a forward() first")
         saved = self._saved
         if _raw_stream(self.device.index) != self._stream:
-            for t in saved[4:]:             # a later forward() must not hand these out before they are read
-                t.record_stream(torch.cuda.current_stream(self.device))
+            # a later forward() drops these, and may hold the last reference to any of them: their memory must not
+            # be handed out before this call has read it
+            for t in saved:
+                if t is not None:
+                    t.record_stream(torch.cuda.current_stream(self.device))
         outs = [self._output(t, name, shape, like) for t, name, shape, like in
                 zip(grads or (None,) * 3, ("dq", "dk", "dv"), (self.shape, self.kv_shape, self.kv_shape), saved)]
         args = (*(None if t is None else t.data_ptr() for t in saved), self._take(dout, "dout", self.shape),

@@ -1,0 +1,63 @@
+"""What the dense layers do on the host around their C calls, on stand-ins for tensors and streams (CPU only)."""
+import pytest
+import torch
+
+from block_sparse_spherical_b200 import abi, api
+
+DEV = torch.device("cuda", 0)
+SHAPE, KV, STREAM = (1, 2, 8, 64), (1, 2, 16, 64), "the current stream"
+
+
+class Stand:
+    """Looks like a contiguous CUDA tensor to a layer; notes the streams it was recorded on."""
+
+    def __init__(self, shape, address, dtype=torch.bfloat16):
+        self.shape, self.address, self.dtype, self.device = torch.Size(shape), address, dtype, DEV
+        self.streams = []
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return self.address
+
+    def record_stream(self, stream):
+        self.streams.append(stream)
+
+
+@pytest.fixture
+def trained(monkeypatch):
+    """A training layer after a forward() on stream 0, its saved tensors, and the C calls it makes from now on."""
+    layer = api.CrossAttentionTrain.__new__(api.CrossAttentionTrain)
+    layer.cfg = abi.BsaCrossConfig(1, 2, 2, 8, 16, 64, abi.BSA_BF16, 0.0)
+    layer.batch, layer.shape, layer.kv_shape, layer.dtype, layer.device = 1, SHAPE, KV, torch.bfloat16, DEV
+    layer.bwd_workspace_bytes, layer._status_ptr = 0, 999
+    saved = (Stand(SHAPE, 1), Stand(KV, 2), Stand(KV, 3), Stand((1,), 4, torch.int32), Stand(SHAPE, 5),
+             Stand(SHAPE[:3], 6, torch.float32), Stand(SHAPE, 7))
+    layer._saved, layer._stream = saved, 0
+    calls = []
+    monkeypatch.setattr(abi, "bsa_cross_attention_backward", lambda *a: calls.append(a[1:]))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: STREAM)
+    monkeypatch.setattr(api, "_raw_stream", lambda index: 0)
+    return layer, saved, calls
+
+
+def grads():
+    return [Stand(SHAPE, 11), Stand(KV, 12), Stand(KV, 13)]
+
+
+def test_backward_passes_what_the_forward_saved(trained):
+    layer, saved, calls = trained
+    out = grads()
+    assert layer.backward(Stand(SHAPE, 10), grads=out) == tuple(out)
+    assert calls == [(1, 2, 3, 4, 5, 6, 7, 10, 11, 12, 13, None, 0, 999, 0)]
+    assert not any(t.streams for t in saved)
+
+
+def test_backward_on_another_stream_records_all_that_was_saved(trained, monkeypatch):
+    """The layer may hold the last reference to q, k, v and key_len too, and drops it at the next forward()."""
+    layer, saved, calls = trained
+    monkeypatch.setattr(api, "_raw_stream", lambda index: 77)
+    layer.backward(Stand(SHAPE, 10), grads=grads())
+    assert calls[0][-1] == 77 and all(t.streams == [STREAM] for t in saved)

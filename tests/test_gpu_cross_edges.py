@@ -68,3 +68,27 @@ def test_a_query_row_that_is_not_finite_gives_nan_over_a_prefix(shape, d, bad):
         assert torch.isnan(out[1, 1, nq // 2]).all()
         out[1, 1, nq // 2] = 0
         assert torch.isfinite(out).all() and layer.check_status() == 0
+
+
+def test_backward_on_another_stream_outlives_inputs_that_only_the_layer_holds():
+    """A forward() that replaces the saved q, k, v and key_len while a backward on a side stream still waits for them:
+    their memory is not handed out to what the first stream allocates next."""
+    shape = (1, 4, 2, 400, 3000, 64)
+    first, second = inputs(*shape, seed=41), inputs(*shape, seed=42)
+    lens, full = lens_of([2999]), lens_of([3000])
+    layer = api.CrossAttentionTrain(1, 4, 400, 3000, 64, kv_heads=2)
+    layer(*first[:3], lens)
+    want = layer.backward(first[3])
+    side, busy = torch.cuda.Stream(), torch.empty(1 << 30, dtype=torch.uint8, device="cuda")
+    for _ in range(5):
+        layer(*(x.clone() for x in first[:3]), lens.clone())         # nobody else keeps these
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            for _ in range(20):
+                busy.fill_(1)
+            got = layer.backward(first[3])
+        layer(*second[:3], full)
+        junk = [torch.full_like(x, NAN) for x in first[:3] for _ in range(3)] + [torch.zeros_like(lens) for _ in range(3)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        del junk
