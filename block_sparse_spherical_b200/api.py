@@ -346,7 +346,7 @@ class CrossAttentionTrain(CrossAttention):
         return out
 
     def backward(self, dout, grads=None):
-        """Gradients (dq, dk, dv) of the last forward() for dL/dout = dout."""
+        """Gradients (dq, dk, dv) of the last forward() for dL/dout = dout; into `grads` where it gives them."""
         if self._saved is None:
             raise RuntimeError("backward() needs a forward() first")
         saved = self._saved
@@ -356,8 +356,11 @@ class CrossAttentionTrain(CrossAttention):
             for t in saved:
                 if t is not None:
                     t.record_stream(torch.cuda.current_stream(self.device))
+        grads = tuple(grads or (None,) * 3)
+        if len(grads) != 3:                 # the C call takes its arguments by position
+            raise ValueError(f"grads must be dq, dk and dv, got {len(grads)} of them")
         outs = [self._output(t, name, shape, like) for t, name, shape, like in
-                zip(grads or (None,) * 3, ("dq", "dk", "dv"), (self.shape, self.kv_shape, self.kv_shape), saved)]
+                zip(grads, ("dq", "dk", "dv"), (self.shape, self.kv_shape, self.kv_shape), saved)]
         args = (*(None if t is None else t.data_ptr() for t in saved), self._take(dout, "dout", self.shape),
                 *(address for _, address in outs))
         self._run(abi.bsa_cross_attention_backward, args, self.bwd_workspace_bytes)

@@ -61,3 +61,20 @@ def test_backward_on_another_stream_records_all_that_was_saved(trained, monkeypa
     monkeypatch.setattr(api, "_raw_stream", lambda index: 77)
     layer.backward(Stand(SHAPE, 10), grads=grads())
     assert calls[0][-1] == 77 and all(t.streams == [STREAM] for t in saved)
+
+
+@pytest.mark.parametrize("count", [1, 2, 4])
+def test_grads_of_another_number_are_refused(trained, count):
+    """With two, every argument behind dk moved up by one: the workspace became dv, and its size an address."""
+    layer, _, calls = trained
+    with pytest.raises(ValueError, match="dq, dk and dv"):
+        layer.backward(Stand(SHAPE, 10), grads=(grads() + grads())[:count])
+    assert not calls
+
+
+def test_grads_may_be_given_in_part(trained, monkeypatch):
+    layer, _, calls = trained
+    dq, dk, dv = grads()
+    monkeypatch.setattr(torch, "empty_like", lambda like: dk)
+    assert layer.backward(Stand(SHAPE, 10), grads=[dq, None, dv]) == (dq, dk, dv)
+    assert calls[0][8:11] == (11, 12, 13)
