@@ -92,13 +92,13 @@ constexpr uint32_t idesc_of(int n, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-// 2^x of two values on the FMA pipe, x <= about 2^8: x = n + f with n = round(x), f in [-1/2, 1/2]; 2^f
-// by the degree-3 minimax polynomial that the block-sparse kernel's route uses too (relative error
-// 7.5e-5, a twentieth of a bf16 rounding's mean), times 2^n. Below -125 it gives 2^-125, where a
-// softmax weight is nothing. NaN gives NaN.
+// 2^x of two values on the FMA pipe, x < 127 (here at most 8, by which a running maximum may lag): x = n + f with
+// n = round(x), f in [-1/2, 1/2]; 2^f by the degree-3 minimax polynomial that the block-sparse kernel's route
+// uses too (relative error 7.5e-5, a twentieth of a bf16 rounding's mean), times 2^n. Below -126.5 n is -127, whose
+// exponent bits are those of 0: exactly 0, also for -inf, as the exponential unit gives. NaN gives NaN.
 __device__ __forceinline__ float2 exp2_fma2(float2 x) {
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-125.f));
-    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-125.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.x) : "f"(-127.f));
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(x.y) : "f"(-127.f));
     const float2 t = __fadd2_rn(x, make_float2(0x1.8p23f, 0x1.8p23f));           // low bits: n
     const float2 n = __fadd2_rn(t, make_float2(-0x1.8p23f, -0x1.8p23f));
     const float2 f = __ffma2_rn(n, make_float2(-1.f, -1.f), x);                 // x - n, exact

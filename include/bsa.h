@@ -320,8 +320,9 @@ BSA_API bsa_status bsa_forward_noalloc(const bsa_config *cfg, const void *q, con
  *   key_len  [batch], nullable (all n_k): entry b attends to its first
  *            key_len[b] states; what lies behind them is never used, whatever
  *            it holds (NaN included). A length of 0 gives zero rows with
- *            lse = -inf and no gradient. A length outside [0, n_k] is clamped
- *            and flagged BSA_ERR_INDEX in *status_word.
+ *            lse = -inf and no gradient, and so does a row all of whose scores
+ *            are -inf. A length outside [0, n_k] is clamped and flagged
+ *            BSA_ERR_INDEX in *status_word.
  *   lse      [batch][heads][n_q] ln Σ_j exp(s·q_i·k_j), nullable: what the
  *            backward needs beside out.
  *   out_low  like out, nullable: what rounding out to bf16 leaves off, as bf16,

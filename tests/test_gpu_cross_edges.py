@@ -92,3 +92,35 @@ def test_backward_on_another_stream_outlives_inputs_that_only_the_layer_holds():
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, want))
         del junk
+
+
+# n_q, n_k: few rows whole and cut, many rows whole and cut
+FORMS = [(2, 300), (2, 20000), (150, 300), (150, 20000)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", FORMS, ids=str)
+def test_rows_whose_scores_are_all_minus_infinity_give_zeros(shape, d):
+    nq, nk = shape
+    q, k, v, _ = inputs(1, 2, 2, nq, nk, d, seed=51)
+    q[0, 1, :, 0] = q[0, 1, :, 0].abs() + 1
+    k[0, 1, :, 0] = -INF
+    layer = api.CrossAttentionTrain(1, 2, nq, nk, d)
+    out = layer(q, k, v)
+    lse = layer._saved[5]
+    assert not out[0, 1].any() and (lse[0, 1] == -INF).all()
+    ref = dense_ref.cross(q[:, :1], k[:, :1], v[:, :1])
+    dense_ref.check(out[:, :1], ref, "out")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", FORMS, ids=str)
+def test_a_weight_that_is_nothing_meets_large_values(shape, d):
+    """Every other pair of keys lies 200 below the rest (a weight of e^-200) and holds values of 3e38."""
+    nq, nk = shape
+    q, k, v, _ = inputs(1, 2, 2, nq, nk, d, seed=52)
+    low = torch.arange(nk, device="cuda") // 2 % 2 == 0
+    q[..., 0] = 16
+    k[..., 0] = torch.where(low, -200 * d ** 0.5 / 16, 0.0).to(BF)
+    v[:, :, low] = 3e38
+    dense_ref.check(api.CrossAttention(1, 2, nq, nk, d)(q, k, v), dense_ref.cross(q, k, v), "out")
