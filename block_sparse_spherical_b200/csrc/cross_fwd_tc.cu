@@ -127,6 +127,7 @@ struct FwdParams {
     FwdPlan plan;
     __nv_bfloat16 *out, *low;   // [rows of all][D]; low: what rounding out leaves off, nullable
     float *lse;             // nullable
+    const __nv_bfloat16 *v; // few rows: for infinite values
     float *part_o, *part_lse, *whole_o, *whole_lse;     // whole: null for a single set
     Cut *cuts;              // [ctas]: single set
     int2 *spans;            // [units]: two sets: first and last CTA of a unit
@@ -568,6 +569,26 @@ __device__ __forceinline__ void end_rows(const FwdParams &p, const Chunk &c, int
     if (c0 == 0 && r.valid && r.lse) *r.lse = l == 0.f ? -CUDART_INF_F : (m + __log2f(l)) * r.lse_unit;
 }
 
+// Few rows: four columns of a row's o that came out NaN although its weights did not. Every lane quarter's product
+// takes all keys of a tile, with a weight of 0 for those of the other quarters, and 0 times an infinite value is
+// NaN. A weight itself is above 0 however far its score lies below the others, so what such a column should
+// hold is the sum of its infinite (and NaN) values, from another look at all of them. y stays where there is
+// none. (v: the four columns of the chunk's first key. Only calls with infinite values come here: 8 rows of
+// 676,000 keys, eight loads in flight, take about 0.3 s, within what the other warps wait.)
+template <int D> __device__ __noinline__ float4 infinite_values(const __nv_bfloat16 *v, int keys, float4 y) {
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [](float &to, uint32_t bits) {          // bits: a bf16 value in the upper half
+        if ((bits & 0x7f800000u) == 0x7f800000u) to += __uint_as_float(bits);
+    };
+#pragma unroll 8
+    for (int j = 0; j < keys; ++j) {
+        const uint2 u = __ldg(reinterpret_cast<const uint2 *>(v + (int64_t)j * D));
+        add(a.x, u.x << 16), add(a.y, u.x & 0xffff0000u), add(a.z, u.y << 16), add(a.w, u.y & 0xffff0000u);
+    }
+    auto pick = [](float y, float a) { return y != y && a != 0.f ? a : y; };
+    return make_float4(pick(y.x, a.x), pick(y.y, a.y), pick(y.z, a.z), pick(y.w, a.w));
+}
+
 template <int D, bool FEW>
 __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, int pl, int hh, int wq, int lane) {
     using C = Cfg<D>;
@@ -777,6 +798,7 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
             if (!(ok = wait_all(&sh.merge_bar, nmerge++ & 1))) break;
             {   // MROWS·D/4 groups of four columns (128 or 256): one a thread
                 const int at = 128 * pl + 32 * wq + lane, mr = at / (D / 4), col = 4 * (at % (D / 4));
+                const float row_l = __shfl_sync(FULL, L, (r0 + mr) & 31);
                 if (mr < C::MROWS && r0 + mr < nrows) {
                     float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -789,6 +811,10 @@ __device__ void softmax_role(const FwdParams &p, Shared<D> &sh, uint32_t tmem, i
                     }
                     const RowOut r = row_out<D>(p, *cp, 0, r0 + mr);
                     if (r.valid) {
+                        if (row_l == row_l && (y.x != y.x || y.y != y.y || y.z != y.z || y.w != y.w)) {
+                            const int64_t key = (cp->z * p.plan.kv_heads + cp->hk) * p.plan.s.n + (int64_t)cp->t0 * kTile;
+                            y = infinite_values<D>(p.v + key * D + col, min(rel, nt * kTile), y);
+                        }
                         if (r.o16) {
                             const uint2 u = make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
                             *reinterpret_cast<uint2 *>(r.o16 + col) = u;
@@ -1257,6 +1283,7 @@ cudaError_t launch_dense_fwd(const DenseProblem &pb, const void *q, const KeySet
         x.out = static_cast<__nv_bfloat16 *>(out);
         x.low = static_cast<__nv_bfloat16 *>(low);
         x.lse = lse;
+        x.v = static_cast<const __nv_bfloat16 *>(sets[k].v);
         x.part_o = ws + L.part_o;
         x.part_lse = ws + L.part_lse;
         if (nsets == 2) {

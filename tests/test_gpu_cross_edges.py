@@ -124,3 +124,39 @@ def test_a_weight_that_is_nothing_meets_large_values(shape, d):
     k[..., 0] = torch.where(low, -200 * d ** 0.5 / 16, 0.0).to(BF)
     v[:, :, low] = 3e38
     dense_ref.check(api.CrossAttention(1, 2, nq, nk, d)(q, k, v), dense_ref.cross(q, k, v), "out")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("shape", FORMS + [(32, 77), (1, 5), (9, 40000)], ids=str)
+def test_infinite_values_give_infinities_in_their_columns(shape, d):
+    """One sign in a column: that infinity in all rows that meet it; both signs, or NaN: NaN. Other columns stay."""
+    nq, nk = shape
+    q, k, v, _ = inputs(2, 2, 1, nq, nk, d, seed=53, size=1.0)
+    lens = [nk, max(1, nk - 150)]
+    v[0, 0, nk // 2, 3], v[0, 0, nk - 1, d - 2] = INF, -INF
+    v[0, 0, 0, 17], v[0, 0, nk - 1, 17] = INF, -INF
+    v[0, 0, nk // 3, 40] = NAN
+    v[1, 0, lens[1]:] = INF                       # not used
+    out = api.CrossAttention(2, 2, nq, nk, d, kv_heads=1)(q, k, v, lens_of(lens))
+    assert (out[0, :, :, 3] == INF).all() and (out[0, :, :, d - 2] == -INF).all()
+    assert torch.isnan(out[0, :, :, [17, 40]]).all()
+    at = [c for c in range(d) if c not in (3, 17, 40, d - 2)]
+    ref = dense_ref.cross(q, k, torch.where(torch.isfinite(v), v, 0), lens)
+    ref = {x: t[..., at] if t.dim() == 4 else t for x, t in ref.items()}
+    dense_ref.check(out[..., at], ref, "out")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq", [1, 5, 40])
+def test_infinite_values_of_a_prefix_and_of_own_states(nq, d):
+    gen = torch.Generator(device="cuda").manual_seed(54)
+    b, npre, nown = 3, 5000, 40
+    q = normal(gen, b, 1, nq, d)
+    kp, vp, ko, vo = (normal(gen, *s) for s in ((1, 1, npre, d), (1, 1, npre, d), (b, 1, nown, d), (b, 1, nown, d)))
+    vp[0, 0, 4000, 6] = INF
+    vo[1, 0, 7, 9] = -INF
+    vo[2, 0, 39, 6] = -INF
+    out = api.PrefixAttention(b, 1, nq, npre, nown, d)(q, kp, vp, ko, vo)
+    assert (out[:2, ..., 6] == INF).all() and torch.isnan(out[2, ..., 6]).all() and (out[1, ..., 9] == -INF).all()
+    out[..., 6], out[1, ..., 9] = 0, 0
+    assert torch.isfinite(out).all()
