@@ -160,3 +160,21 @@ def test_infinite_values_of_a_prefix_and_of_own_states(nq, d):
     assert (out[:2, ..., 6] == INF).all() and torch.isnan(out[2, ..., 6]).all() and (out[1, ..., 9] == -INF).all()
     out[..., 6], out[1, ..., 9] = 0, 0
     assert torch.isfinite(out).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq", [128, 1, 150, 333])
+def test_an_infinite_key_without_weight_has_no_gradient(nq, d):
+    """Scores of -inf with every row (and so a weight of 0): dk and dv are 0 there whether or not the rows fill their
+    last tile, and those of the other keys are what they are without it."""
+    q, k, v, g = inputs(1, 2, 2, nq, 300, d, seed=55)
+    q[..., 0] = q[..., 0].abs() + 1
+    k[:, :, 77, 0] = -INF
+    layer = api.CrossAttentionTrain(1, 2, nq, 300, d)
+    out = layer(q, k, v)
+    _, dk, dv = layer.backward(g)                     # dq is 0 times infinity in that column
+    assert not dk[:, :, 77].any() and not dv[:, :, 77].any()
+    rest = [j for j in range(300) if j != 77]
+    ref = dense_ref.cross(q, k[:, :, rest], v[:, :, rest], dout=g)
+    for name, x in (("out", out), ("dk", dk[:, :, rest]), ("dv", dv[:, :, rest])):
+        dense_ref.check(x, ref, name)
