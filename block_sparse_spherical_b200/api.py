@@ -287,6 +287,12 @@ class _DenseLayer:
         call(self.cfg, *args, None if ws is None else ws.data_ptr(), workspace_bytes, self._status_ptr,
              _raw_stream(self.device.index))
 
+    def _capturing(self) -> bool:
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                return torch.cuda.is_current_stream_capturing()
+        return torch.cuda.is_current_stream_capturing()
+
     def check_status(self) -> int:
         """Synchronise and return the kernels' status code (0 = OK); resets it."""
         with torch.cuda.device(self.device):
@@ -327,13 +333,16 @@ class CrossAttentionTrain(CrossAttention):
 
     forward(q, k, v, key_len) -> out; backward(dout) -> (dq, dk, dv) of the last forward(). Its q, k, v,
     key_len and out are kept by reference until then and have to stay as they are (and with them, of
-    the layer's own, the rows' log-sum-exp and what rounding out to bf16 left off).
+    the layer's own, the rows' log-sum-exp and what rounding out to bf16 left off). A backward() captured
+    into a graph reads them in every replay: what a forward() outside of a capture saved is then kept as
+    long as the layer is.
     """
 
     def __init__(self, *args, **kw):
         super().__init__(*args, **kw)
         self.bwd_workspace_bytes = abi.bsa_cross_backward_workspace_size(self.cfg)
         self._saved = None
+        self._replayed = []                 # what captured backwards read and no graph's memory pool holds
 
     def __call__(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
         return self.forward(q, k, v, key_len, out)
@@ -343,6 +352,7 @@ class CrossAttentionTrain(CrossAttention):
         low = torch.empty_like(q)
         out = self._forward(q, k, v, key_len, out, lse, low)
         self._saved, self._stream = (q, k, v, key_len, out, lse, low), _raw_stream(self.device.index)
+        self._captured = self._capturing()
         return out
 
     def backward(self, dout, grads=None):
@@ -356,6 +366,8 @@ class CrossAttentionTrain(CrossAttention):
             for t in saved:
                 if t is not None:
                     t.record_stream(torch.cuda.current_stream(self.device))
+        if not self._captured and self._capturing():
+            self._replayed.append(saved)
         grads = tuple(grads or (None,) * 3)
         if len(grads) != 3:                 # the C call takes its arguments by position
             raise ValueError(f"grads must be dq, dk and dv, got {len(grads)} of them")

@@ -1,4 +1,7 @@
 """What the dense layers do on the host around their C calls, on stand-ins for tensors and streams (CPU only)."""
+import gc
+import weakref
+
 import pytest
 import torch
 
@@ -34,11 +37,12 @@ def trained(monkeypatch):
     layer.bwd_workspace_bytes, layer._status_ptr = 0, 999
     saved = (Stand(SHAPE, 1), Stand(KV, 2), Stand(KV, 3), Stand((1,), 4, torch.int32), Stand(SHAPE, 5),
              Stand(SHAPE[:3], 6, torch.float32), Stand(SHAPE, 7))
-    layer._saved, layer._stream = saved, 0
+    layer._saved, layer._stream, layer._captured, layer._replayed = saved, 0, False, []
     calls = []
     monkeypatch.setattr(abi, "bsa_cross_attention_backward", lambda *a: calls.append(a[1:]))
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: STREAM)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(api, "_raw_stream", lambda index: 0)
     return layer, saved, calls
 
@@ -78,3 +82,20 @@ def test_grads_may_be_given_in_part(trained, monkeypatch):
     monkeypatch.setattr(torch, "empty_like", lambda like: dk)
     assert layer.backward(Stand(SHAPE, 10), grads=[dq, None, dv]) == (dq, dk, dv)
     assert calls[0][8:11] == (11, 12, 13)
+
+
+@pytest.mark.parametrize("forward_captured", [False, True])
+def test_a_captured_backward_keeps_what_an_eager_forward_saved(trained, monkeypatch, forward_captured):
+    """A graph's replays read it, also after a later forward() took its place. What a captured forward saved lies in
+    that graph's own memory and is not kept twice."""
+    layer, saved, _ = trained
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    layer._captured = forward_captured
+    layer.backward(Stand(SHAPE, 10), grads=grads())
+    seen = [weakref.ref(t) for t in saved]
+    saved = layer._saved = None
+    trained = None
+    gc.collect()
+    assert len(layer._replayed) == (0 if forward_captured else 1)
+    if not forward_captured:
+        assert all(r() is not None for r in seen)

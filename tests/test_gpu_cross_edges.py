@@ -178,3 +178,30 @@ def test_an_infinite_key_without_weight_has_no_gradient(nq, d):
     ref = dense_ref.cross(q, k[:, :, rest], v[:, :, rest], dout=g)
     for name, x in (("out", out), ("dk", dk[:, :, rest]), ("dv", dv[:, :, rest])):
         dense_ref.check(x, ref, name)
+
+
+def test_a_backward_captured_alone_replays_after_later_forwards():
+    """An eager forward, its backward in a graph: replays read the rows' statistics of that forward, which only the
+    layer holds, with other calls and allocations in between."""
+    q, k, v, g = inputs(2, 4, 2, 130, 1000, 128, seed=43)
+    lens = lens_of([1000, 301])
+    layer = api.CrossAttentionTrain(2, 4, 130, 1000, 128, kv_heads=2)
+    layer(q, k, v, lens)
+    layer.backward(g)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        grads = layer.backward(g)
+    for seed in range(3):
+        other = inputs(2, 4, 2, 130, 1000, 128, seed=60 + seed)
+        junk = []
+        for _ in range(3):
+            layer(*other[:3])
+            junk.append([torch.full(s, NAN, dtype=t, device="cuda") for s, t in
+                         ((layer.shape, BF), (layer.shape[:3], torch.float32), (layer.shape, BF))])
+        g.copy_(other[3])
+        graph.replay()
+        ref = dense_ref.cross(q, k, v, [1000, 301], dout=g)
+        for name, x in zip(("dq", "dk", "dv"), grads):
+            dense_ref.check(x, ref, name)
+        del junk
