@@ -57,6 +57,30 @@ bsa_status check_workspace(const void *workspace, size_t have, size_t need) {
     return aligned(workspace, 256) ? BSA_OK : BSA_ERR_ALIGNMENT;
 }
 
+// The memory of a call's arguments. Whatever a kernel writes may meet nothing else of the call: tiles are read and
+// rows written in no fixed order.
+struct Extent {
+    const void *at;         // null: not given
+    size_t bytes;
+};
+template <size_t N, size_t M> bool apart(const Extent (&written)[N], const Extent (&read)[M]) {
+    auto meet = [](const Extent &a, const Extent &b) {
+        const uintptr_t x = (uintptr_t)a.at, y = (uintptr_t)b.at;
+        return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+    };
+    for (size_t i = 0; i < N; ++i) {
+        for (size_t j = i + 1; j < N; ++j)
+            if (meet(written[i], written[j])) return false;
+        for (const Extent &r : read)
+            if (meet(written[i], r)) return false;
+    }
+    return true;
+}
+// Bytes of the query rows' tensors and of a set's keys.
+size_t q_bytes(const DenseProblem &p) { return (size_t)(p.batch * p.kv_heads * p.rows * p.d) * 2; }
+size_t set_bytes(const DenseProblem &p, const KeySet &s) { return (size_t)(s.sets * p.kv_heads * s.n * p.d) * 2; }
+size_t len_bytes(const KeySet &s) { return (size_t)s.sets * 4; }
+
 KeySet cross_set(const bsa_cross_config *c, const void *k, const void *v, const int32_t *len) {
     return KeySet{k, v, len, c->n_k, c->batch, 1};
 }
@@ -105,11 +129,16 @@ bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const
         if (x == out || x == out_low) return BSA_ERR_INVALID_ARG;
     if (out_low == out) return BSA_ERR_INVALID_ARG;
     const KeySet s = cross_set(cfg, k, v, key_len);
-    const bsa_status ws = check_workspace(workspace, workspace_bytes, fwd_bytes(p, &s, 1));
+    const size_t need = fwd_bytes(p, &s, 1);
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, need);
     if (ws != BSA_OK) return ws;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
         !aligned(out_low, 16) || !aligned(key_len, 4) || !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
+    const size_t rows = q_bytes(p), keys = set_bytes(p, s);
+    if (!apart({{out, rows}, {out_low, rows}, {lse, rows / p.d * 2}, {workspace, need}, {status_word, 4}},
+               {{q, rows}, {k, keys}, {v, keys}, {key_len, len_bytes(s)}}))
+        return BSA_ERR_INVALID_ARG;
     return from_cuda(bsa::launch_dense_fwd(p, q, &s, 1, out, out_low, lse, static_cast<float *>(workspace), status_word, stream));
 }
 
@@ -140,13 +169,18 @@ bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void 
         if (grads[i] == out_low) return BSA_ERR_INVALID_ARG;
     }
     const KeySet s = cross_set(cfg, k, v, key_len);
-    const bsa_status ws = check_workspace(workspace, workspace_bytes, bwd_bytes(p, s));
+    const size_t need = bwd_bytes(p, s);
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, need);
     if (ws != BSA_OK) return ws;
     for (int i = 0; i < 5; ++i)
         if (!aligned(in[i], 16)) return BSA_ERR_ALIGNMENT;
     if (!aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(out_low, 16) || !aligned(lse, 4) || !aligned(key_len, 4) ||
         !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
+    const size_t rows = q_bytes(p), keys = set_bytes(p, s);
+    if (!apart({{dq, rows}, {dk, keys}, {dv, keys}, {workspace, need}, {status_word, 4}},
+               {{q, rows}, {k, keys}, {v, keys}, {key_len, len_bytes(s)}, {out, rows}, {lse, rows / p.d * 2}, {out_low, rows}, {dout, rows}}))
+        return BSA_ERR_INVALID_ARG;
     return from_cuda(bsa::launch_dense_bwd(p, q, s, out, out_low, lse, dout, dq, dk, dv, static_cast<float *>(workspace), status_word,
                                            stream));
 }
@@ -175,12 +209,18 @@ bsa_status bsa_prefix_attention(const bsa_prefix_config *cfg, const void *q, con
     if (!out) return BSA_ERR_INVALID_ARG;
     KeySet sets[2];
     prefix_sets(cfg, k_prefix, v_prefix, prefix_len, k_own, v_own, own_len, sets);
-    const bsa_status ws = check_workspace(workspace, workspace_bytes, fwd_bytes(p, sets, 2));
+    const size_t need = fwd_bytes(p, sets, 2);
+    const bsa_status ws = check_workspace(workspace, workspace_bytes, need);
     if (ws != BSA_OK) return ws;
     for (const void *x : in)
         if (!aligned(x, 16)) return BSA_ERR_ALIGNMENT;
     if (!aligned(out, 16) || !aligned(prefix_len, 4) || !aligned(own_len, 4) || !aligned(status_word, 4))
         return BSA_ERR_ALIGNMENT;
+    const size_t rows = q_bytes(p), shared = set_bytes(p, sets[0]), own = set_bytes(p, sets[1]);
+    if (!apart({{out, rows}, {workspace, need}, {status_word, 4}},
+               {{q, rows}, {k_prefix, shared}, {v_prefix, shared}, {prefix_len, len_bytes(sets[0])}, {k_own, own}, {v_own, own},
+                {own_len, len_bytes(sets[1])}}))
+        return BSA_ERR_INVALID_ARG;
     return from_cuda(
         bsa::launch_dense_fwd(p, q, sets, 2, out, nullptr, nullptr, static_cast<float *>(workspace), status_word, stream));
 }

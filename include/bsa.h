@@ -338,7 +338,9 @@ BSA_API bsa_status bsa_forward_noalloc(const bsa_config *cfg, const void *q, con
  * split when there are few query rows. Every call rewrites what it reads of
  * it; calls that overlap on the GPU need workspaces of their own. status_word:
  * nullable device uint32, OR-ed, read by bsa_check_status. Results do not
- * depend on the order in which the GPU runs the parts.
+ * depend on the order in which the GPU runs the parts. What a call writes
+ * (results, workspace, status_word) may share no byte with anything else it is
+ * given: BSA_ERR_INVALID_ARG.
  */
 typedef struct {
     int32_t batch;          /* B >= 1 */

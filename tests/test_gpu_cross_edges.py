@@ -205,3 +205,28 @@ def test_a_backward_captured_alone_replays_after_later_forwards():
         for name, x in zip(("dq", "dk", "dv"), grads):
             dense_ref.check(x, ref, name)
         del junk
+
+
+def test_outputs_that_share_memory_are_refused_and_neighbours_are_not():
+    """One buffer for all tensors of a call, end to end; then with an output moved by 16 bytes onto its neighbour."""
+    b, h, nq, nk, d = 2, 2, 40, 300, 64
+    q, k, v, g = inputs(b, h, h, nq, nk, d, seed=44)
+    layer = api.CrossAttentionTrain(b, h, nq, nk, d)
+    want = [layer(q, k, v), *layer.backward(g)]
+    buf = torch.zeros(4 * q.numel() + 4 * k.numel(), dtype=BF, device="cuda")
+    at, views = 0, []
+    for x in (q, k, v, g, q, q, k, v):                     # q k v dout, out dq dk dv
+        views.append(buf[at:at + x.numel()].view(x.shape))
+        at += x.numel()
+    for x, y in zip(views, (q, k, v, g)):
+        x.copy_(y)
+    got = [layer(*views[:3], out=views[4]), *layer.backward(views[3], grads=views[5:])]
+    assert all(torch.equal(x, y) for x, y in zip(got, want)) and layer.check_status() == 0
+    shifted = buf[3 * q.numel() + 2 * k.numel() - 8:][:q.numel()].view(q.shape)    # dq, 16 bytes into out
+    with pytest.raises(abi.BsaError) as e:
+        layer.backward(views[3], grads=[shifted, *views[6:]])
+    assert e.value.code == 1
+    shifted = buf[3 * q.numel():][:q.numel()].view(q.shape)                        # inside k
+    with pytest.raises(abi.BsaError) as e:
+        layer(*views[:3], out=shifted)
+    assert e.value.code == 1
