@@ -294,7 +294,9 @@ class _DenseLayer:
         return torch.cuda.is_current_stream_capturing()
 
     def check_status(self) -> int:
-        """Synchronise and return the kernels' status code (0 = OK); resets it."""
+        """Synchronise the device (a layer's calls may be on any of its streams) and return the kernels'
+        status code (0 = OK); resets it."""
+        torch.cuda.synchronize(self.device)
         with torch.cuda.device(self.device):
             return abi.bsa_check_status(self.status)
 

@@ -1,4 +1,5 @@
 """What the dense layers do on the host around their C calls, on stand-ins for tensors and streams (CPU only)."""
+import contextlib
 import gc
 import weakref
 
@@ -99,3 +100,13 @@ def test_a_captured_backward_keeps_what_an_eager_forward_saved(trained, monkeypa
     assert len(layer._replayed) == (0 if forward_captured else 1)
     if not forward_captured:
         assert all(r() is not None for r in seen)
+
+
+def test_check_status_waits_for_all_streams(trained, monkeypatch):
+    layer, _, _ = trained
+    order = []
+    layer.status = "word"
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: order.append(device))
+    monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
+    monkeypatch.setattr(abi, "bsa_check_status", lambda word: order.append(word) or 7)
+    assert layer.check_status() == 7 and order == [DEV, "word"]

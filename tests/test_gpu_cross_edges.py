@@ -230,3 +230,17 @@ def test_outputs_that_share_memory_are_refused_and_neighbours_are_not():
     with pytest.raises(abi.BsaError) as e:
         layer(*views[:3], out=shifted)
     assert e.value.code == 1
+
+
+def test_a_bad_length_on_a_busy_stream_is_reported():
+    q, k, v, _ = inputs(2, 2, 2, 40, 200, 64, seed=45)
+    layer = api.CrossAttention(2, 2, 40, 200, 64)
+    busy, side = torch.empty(1 << 30, dtype=torch.uint8, device="cuda"), torch.cuda.Stream()
+    bad = lens_of([201, 5])
+    layer(q, k, v, lens_of([200, 5]))             # (the first call of a kernel waits for the device by itself)
+    assert layer.check_status() == 0
+    with torch.cuda.stream(side):
+        for _ in range(50):
+            busy.fill_(1)
+        layer(q, k, v, bad)
+    assert layer.check_status() == 7 and layer.check_status() == 0
