@@ -162,7 +162,7 @@ class BSATrain(BSA):
         self.lse_fine = torch.empty((b, h, n, 2), dtype=torch.float32, device=dev)
         self.bwd_workspace_bytes = abi.bsa_backward_workspace_size(self.cfg)
         self.bwd_workspace = torch.zeros(self.bwd_workspace_bytes, dtype=torch.uint8, device=dev)
-        self._saved = self._stream = None
+        self._saved = None
 
     def __call__(self, q, k, v, gates, out=None) -> torch.Tensor:
         return self.forward(q, k, v, gates, out)
@@ -343,7 +343,8 @@ class CrossAttentionTrain(CrossAttention):
     def __init__(self, *args, **kw):
         super().__init__(*args, **kw)
         self.bwd_workspace_bytes = abi.bsa_cross_backward_workspace_size(self.cfg)
-        self._saved = None
+        self._saved = self._stream = None
+        self._captured = False
         self._replayed = []                 # what captured backwards read and no graph's memory pool holds
 
     def __call__(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
