@@ -352,7 +352,7 @@ class CrossAttentionTrain(CrossAttention):
 
     def forward(self, q, k, v, key_len=None, out=None) -> torch.Tensor:
         lse = torch.empty(self.shape[:3], dtype=torch.float32, device=self.device)
-        low = torch.empty_like(q)
+        low = torch.empty(self.shape, dtype=self.dtype, device=self.device)
         out = self._forward(q, k, v, key_len, out, lse, low)
         self._saved, self._stream = (q, k, v, key_len, out, lse, low), _raw_stream(self.device.index)
         self._captured = self._capturing()

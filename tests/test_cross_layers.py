@@ -110,3 +110,13 @@ def test_check_status_waits_for_all_streams(trained, monkeypatch):
     monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
     monkeypatch.setattr(abi, "bsa_check_status", lambda word: order.append(word) or 7)
     assert layer.check_status() == 7 and order == [DEV, "word"]
+
+
+@pytest.mark.parametrize("q", [None, [1.0], "q"])
+def test_forward_refuses_what_is_no_tensor_as_serving_does(trained, monkeypatch, q):
+    layer, _, _ = trained
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda shape, dtype, device: empty(shape, dtype=dtype))
+    for call in (layer.forward, super(type(layer), layer).__call__):
+        with pytest.raises(ValueError, match="q must be a CUDA tensor"):
+            call(q, Stand(KV, 2), Stand(KV, 3))
