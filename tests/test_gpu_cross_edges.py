@@ -244,3 +244,38 @@ def test_a_bad_length_on_a_busy_stream_is_reported():
             busy.fill_(1)
         layer(q, k, v, bad)
     assert layer.check_status() == 7 and layer.check_status() == 0
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [0.0, 30.0])
+@pytest.mark.parametrize("nq", [1, 7, 150])
+@pytest.mark.parametrize("nk", [700, 9000])
+def test_flat_and_peaked_rows_in_cut_units(nq, nk, size, d):
+    """Logits in the hundreds that grow along the keys, in either order: the running maximum moves from tile to tile by
+    more than it may lag, and parts of a unit lie far apart; or all logits equal."""
+    q, k, v, g = inputs(1, 2, 1, nq, nk, d, seed=46, size=size)
+    ramp = torch.linspace(0.1, 2.0, nk, device="cuda")[:, None]
+    for r in (ramp, ramp.flip(0)):
+        kr = (k.float() * r).to(BF)
+        ref = dense_ref.cross(q, kr, v, dout=g)
+        layer = api.CrossAttentionTrain(1, 2, nq, nk, d, kv_heads=1)
+        dense_ref.check(layer(q, kr, v), ref, "out")
+        dense_ref.check(layer._saved[5], ref, "lse")
+        for name, x in zip(("dq", "dk", "dv"), layer.backward(g)):
+            dense_ref.check(x, ref, name)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nq", [1, 5, 100])
+@pytest.mark.parametrize("large", ["own", "prefix"])
+def test_prefix_and_own_states_far_apart(large, nq, d):
+    gen = torch.Generator(device="cuda").manual_seed(47)
+    b, npre, nown = 4, 9000, 300
+    q = normal(gen, b, 2, nq, d, size=2.0)
+    kp, vp, ko, vo = (normal(gen, *s) for s in ((1, 1, npre, d), (1, 1, npre, d), (b, 1, nown, d), (b, 1, nown, d)))
+    (ko if large == "own" else kp).mul_(40)
+    layer = api.PrefixAttention(b, 2, nq, npre, nown, d, kv_heads=1)
+    for own in (None, [300, 0, 1, 129]):
+        out = layer(q, kp, vp, ko, vo, own_len=lens_of(own))
+        dense_ref.check(out, dense_ref.prefix(q, kp, vp, ko, vo, None, own), "out")
+    assert layer.check_status() == 0
