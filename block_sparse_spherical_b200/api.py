@@ -246,6 +246,7 @@ class _DenseLayer:
     """
 
     def __init__(self, batch, heads, kv_heads, head_dim, dtype, scale, device):
+        # float32 is a type of the library that these operators lack: the C call refuses it (BSA_ERR_UNSUPPORTED)
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError(f"dtype must be bfloat16, got {dtype}")
         self.kv_heads = heads if kv_heads is None else kv_heads

@@ -1,6 +1,7 @@
 // C ABI of cross attention, its backward and shared-prefix attention (declared
 // in include/bsa.h): argument validation, workspace layout and dispatch. No
-// allocation, no synchronisation, no global state.
+// allocation, no synchronisation, no state beyond the driver's entry point for
+// tensor maps and a note of the devices on which a kernel has been set up.
 #include <math.h>
 
 #include "cross.cuh"

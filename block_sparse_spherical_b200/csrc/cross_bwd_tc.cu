@@ -29,10 +29,13 @@
 // and dv (2.4e-3) have no columns of tensor memory left for it. D's own error would be common to
 // a row's dS: from out alone, which is rounded, it took dq and dk to 2.8e-3 at 64 keys.
 //
-// What bounds it: 12288 x 12288, 8 heads, D = 64: both passes 1,365 us (alone: dk and dv 718, dq 650),
-// the row pass 9, the parts' sum 6; 10 n² d flops a head are 773 GFLOP, 0.56 PFLOP/s of them in 1.39 ms. A step of 128 x 128 needs 1,024
-// clocks of the exponential unit and about as many of the tensor cores; what it takes (2,400) is the chain
-// S, exponentials, P, dP, dS, product, of which only parts overlap in the tensor memory there is.
+// What bounds it (here and below: GPU time of calls on the same inputs): 12288 x 12288, 8 heads, D = 64: both passes
+// 1,250 to 1,390 us, with the data and the clock (launched alone, at the slower end: dk and dv 718, dq 650), the row
+// pass 10, the parts' sum 7; 10 n² d flops a head are 773 GFLOP for the 8 heads, 0.56 to 0.62 PFLOP/s. D = 128,
+// 4 heads: 977 us, 0.79 PFLOP/s. Tensor pipe and exponential unit are each 46 % busy (D = 128: 60 % and 30 %). At
+// D = 64 a step of 128 x 128 needs 1,024 clocks of the exponential unit and about as many of the tensor cores; what
+// it takes (2,400) is the chain S, exponentials, P, dP, dS, product, of which only parts overlap in the tensor
+// memory there is.
 //
 // One persistent CTA per SM, 640 threads: warp 0 finds the units, hands them out and copies their tiles,
 // warp 1 issues S and dP, warp 2 P·B1 (KEY), warp 3 dS·B0 (one thread issues a tcgen05 instruction
@@ -534,8 +537,8 @@ __device__ void softmax_role(const BwdParams &p, Shared<D> &sh, uint32_t tmem, i
                     x[16 * h + 2 * e + 1] = e2[e].y;
                 }
             }
-            // this thread's columns that count (KEY: read anew in each step, 1,647 us for a training step of 12288 x 12288,
-            // 8 heads, D = 64, in a graph; with a register for it over the loop 1,656, without this mask 1,635)
+            // this thread's columns that count (KEY: read anew in each step, 1,645 us for a training step of 12288 x 12288,
+            // 8 heads, D = 64; with a register for it over the loop 1,656, without this mask 1,635)
             const int valid = (KEY ? *(volatile const int *)&cp->cols : cols) - t * kTile - 32 * w;
             if (KEY && !counts) {
 #pragma unroll

@@ -44,11 +44,17 @@
 // is bf16: each half a step, together 2.3e-3 of out's norm from 64 bits, where rounding out alone gives
 // 1.7e-3. out_low carries what rounding out leaves off to the backward's row sums.
 //
-// What bounds it and what it takes: 12288 rows a head, 8 heads, on 29040 keys, D = 64: 920 us, 0.79 PFLOP/s; the
-// exponential unit alone needs 634 us of that (16 a clock and SM), a step of 256 rows and 128 keys takes
-// 1.55 us, the rest being the chain S, maximum, exponentials, P, P·V of each pipeline where the
-// other does not cover it. 12288 on 12288: 450 us. Few rows: 24 entries of one row, 16 heads on
-// 4 key heads, D = 128, 29040 keys: 211 us, the keys' and values' 1.43 GB at the rate of memory, 6.8 TB/s.
+// What it takes (here and below: GPU time of calls on the same inputs in a graph; "a call": of the Python layer, on
+// three sets of inputs in turn) and what bounds it:
+//   12288 rows a head, 8 heads, on 29040 keys, D = 64: 920 to 955 us, 0.77 to 0.79 PFLOP/s (a call 1,005); 12288
+//   on 12288: 400 to 450. The exponential unit alone needs 634 us of the first (16 a clock and SM) and is 64 %
+//   busy, the tensor pipe 37 %, instructions issue in 65 % of all cycles: a step of 256 rows and 128 keys takes
+//   1.55 us, the rest being issue and the chain S, maximum, exponentials, P, P·V of each pipeline where the
+//   other does not cover it.
+//   D = 128, 4 heads, 12288 on 12288: 281 us, 1.10 PFLOP/s; 8 heads on 29040 keys 1,365 us, 1.07. Tensor pipe and
+//   exponential unit are both 53 % busy: the chain again, with half-tile steps in the tensor memory there is.
+//   Few rows: 24 entries of one row, 16 heads on 4 key heads, D = 128, 29040 keys: 212 us for 1.43 GB of keys and
+//   values, 6.75 TB/s, of which L2 holds some from call to call; a call 244 us, 5.85 TB/s.
 //
 // Every wait on an mbarrier is bounded (2 s), as in the block-sparse kernel.
 #include <math_constants.h>
@@ -573,8 +579,9 @@ __device__ __forceinline__ void end_rows(const FwdParams &p, const Chunk &c, int
 // takes all keys of a tile, with a weight of 0 for those of the other quarters, and 0 times an infinite value is
 // NaN. A weight itself is above 0 however far its score lies below the others, so what such a column should
 // hold is the sum of its infinite (and NaN) values, from another look at all of them. y stays where there is
-// none. (v: the four columns of the chunk's first key. Only calls with infinite values come here: 8 rows of
-// 676,000 keys, eight loads in flight, take about 0.3 s, within what the other warps wait.)
+// none. (v: the four columns of the chunk's first key. Only calls with infinite values come here. Eight loads are in
+// flight: 32 rows, D = 128, on 40 million keys, 270,000 a CTA, take 149 ms instead of 2.9, within the 2 s that
+// the other warps wait.)
 template <int D> __device__ __noinline__ float4 infinite_values(const __nv_bfloat16 *v, int keys, float4 y) {
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [](float &to, uint32_t bits) {          // bits: a bf16 value in the upper half
