@@ -25,7 +25,9 @@ EXPORTS = ("bsa_pool", "bsa_compress_select", "bsa_compress_select_ws", "bsa_fin
            "bsa_latlon_healpix_plan", "bsa_latlon_workspace_size", "bsa_latlon_to_healpix", "bsa_forward_mirrored",
            "bsa_cross_workspace_size", "bsa_cross_attention", "bsa_cross_backward_workspace_size",
            "bsa_cross_attention_backward", "bsa_prefix_workspace_size", "bsa_prefix_attention")
-TESTING_EXPORTS = ("bsa_testing_fine_attention_withhold", "bsa_testing_exp2", "bsa_testing_mma_rate")
+TESTING_EXPORTS = ("bsa_testing_fine_attention_withhold", "bsa_testing_exp2", "bsa_testing_mma_rate",
+                   "bsa_testing_cross_attention_withhold", "bsa_testing_cross_attention_backward_withhold",
+                   "bsa_testing_prefix_attention_withhold")
 
 
 class BsaConfig(ctypes.Structure):
@@ -92,6 +94,9 @@ def load() -> ctypes.CDLL:
         "bsa_prefix_workspace_size": [Y, ctypes.POINTER(ctypes.c_size_t)],
         "bsa_prefix_attention": [Y, P, P, P, P, P, P, P, P, P, S, P, P],
         "bsa_testing_fine_attention_withhold": [C, P, P, P, P, P, P, P, P, ctypes.c_int64, P],
+        "bsa_testing_cross_attention_withhold": [X, P, P, P, P, P, P, P, P, S, P, P, ctypes.c_int64],
+        "bsa_testing_cross_attention_backward_withhold": [X, P, P, P, P, P, P, P, P, P, P, P, P, S, P, P, ctypes.c_int64],
+        "bsa_testing_prefix_attention_withhold": [Y, P, P, P, P, P, P, P, P, P, S, P, P, ctypes.c_int64],
         "bsa_testing_exp2": [P, P, ctypes.c_int64, ctypes.c_int32, P],
         "bsa_testing_mma_rate": [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P],
     }

@@ -12,6 +12,8 @@ struct DenseProblem {
     int64_t batch, heads, kv_heads, n_q, d;
     int64_t rows;           // (heads / kv_heads) * n_q: rows of a batch entry and key head
     float scale;
+    int64_t withhold = -1;  // test hook: the copy of this number in the order of a CTA (key and value tiles; backward:
+                            // steps) is not issued by the first CTA of each pass; -1: off
 };
 
 // One set of keys for the rows of a forward pass. The rows of a batch entry

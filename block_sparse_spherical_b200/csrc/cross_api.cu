@@ -4,6 +4,7 @@
 // tensor maps and a note of the devices on which a kernel has been set up.
 #include <math.h>
 
+#include "bsa_testing.h"
 #include "cross.cuh"
 
 namespace {
@@ -105,26 +106,14 @@ size_t bwd_bytes(const DenseProblem &p, KeySet s) {
     return bsa::dense_bwd_floats(p, s) * sizeof(float);
 }
 
-}  // namespace
-
-extern "C" {
-
-bsa_status bsa_cross_workspace_size(const bsa_cross_config *cfg, size_t *bytes) {
+// The calls; `withhold`: a test hook (cross.cuh), -1 for the library's own.
+bsa_status cross_forward(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
+                         const int32_t *key_len, void *out, float *lse, void *out_low, void *workspace,
+                         size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream, int64_t withhold) {
     DenseProblem p;
     const bsa_status st = make_cross(cfg, &p);
     if (st != BSA_OK) return st;
-    if (!bytes) return BSA_ERR_INVALID_ARG;
-    const KeySet s = cross_set(cfg, nullptr, nullptr, nullptr);
-    *bytes = fwd_bytes(p, &s, 1);
-    return BSA_OK;
-}
-
-bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
-                               const int32_t *key_len, void *out, float *lse, void *out_low, void *workspace,
-                               size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream) {
-    DenseProblem p;
-    const bsa_status st = make_cross(cfg, &p);
-    if (st != BSA_OK) return st;
+    p.withhold = withhold;
     if (!q || !k || !v || !out) return BSA_ERR_INVALID_ARG;
     for (const void *x : {q, k, v})
         if (x == out || x == out_low) return BSA_ERR_INVALID_ARG;
@@ -143,22 +132,14 @@ bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const
     return from_cuda(bsa::launch_dense_fwd(p, q, &s, 1, out, out_low, lse, static_cast<float *>(workspace), status_word, stream));
 }
 
-bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t *bytes) {
+bsa_status cross_backward(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
+                          const int32_t *key_len, const void *out, const float *lse, const void *out_low,
+                          const void *dout, void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes,
+                          uint32_t *status_word, cudaStream_t stream, int64_t withhold) {
     DenseProblem p;
     const bsa_status st = make_cross(cfg, &p);
     if (st != BSA_OK) return st;
-    if (!bytes) return BSA_ERR_INVALID_ARG;
-    *bytes = bwd_bytes(p, cross_set(cfg, nullptr, nullptr, nullptr));
-    return BSA_OK;
-}
-
-bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
-                                        const int32_t *key_len, const void *out, const float *lse, const void *out_low,
-                                        const void *dout, void *dq, void *dk, void *dv, void *workspace,
-                                        size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream) {
-    DenseProblem p;
-    const bsa_status st = make_cross(cfg, &p);
-    if (st != BSA_OK) return st;
+    p.withhold = withhold;
     const void *in[] = {q, k, v, out, dout, lse};
     void *grads[] = {dq, dk, dv};
     for (const void *x : in)
@@ -186,24 +167,14 @@ bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void 
                                            stream));
 }
 
-bsa_status bsa_prefix_workspace_size(const bsa_prefix_config *cfg, size_t *bytes) {
+bsa_status prefix_forward(const bsa_prefix_config *cfg, const void *q, const void *k_prefix, const void *v_prefix,
+                          const int32_t *prefix_len, const void *k_own, const void *v_own, const int32_t *own_len,
+                          void *out, void *workspace, size_t workspace_bytes, uint32_t *status_word,
+                          cudaStream_t stream, int64_t withhold) {
     DenseProblem p;
     const bsa_status st = make_prefix(cfg, &p);
     if (st != BSA_OK) return st;
-    if (!bytes) return BSA_ERR_INVALID_ARG;
-    KeySet sets[2];
-    prefix_sets(cfg, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, sets);
-    *bytes = fwd_bytes(p, sets, 2);
-    return BSA_OK;
-}
-
-bsa_status bsa_prefix_attention(const bsa_prefix_config *cfg, const void *q, const void *k_prefix, const void *v_prefix,
-                                const int32_t *prefix_len, const void *k_own, const void *v_own, const int32_t *own_len,
-                                void *out, void *workspace, size_t workspace_bytes, uint32_t *status_word,
-                                cudaStream_t stream) {
-    DenseProblem p;
-    const bsa_status st = make_prefix(cfg, &p);
-    if (st != BSA_OK) return st;
+    p.withhold = withhold;
     const void *in[] = {q, k_prefix, v_prefix, k_own, v_own};
     for (const void *x : in)
         if (!x || x == out) return BSA_ERR_INVALID_ARG;
@@ -224,6 +195,89 @@ bsa_status bsa_prefix_attention(const bsa_prefix_config *cfg, const void *q, con
         return BSA_ERR_INVALID_ARG;
     return from_cuda(
         bsa::launch_dense_fwd(p, q, sets, 2, out, nullptr, nullptr, static_cast<float *>(workspace), status_word, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+bsa_status bsa_cross_workspace_size(const bsa_cross_config *cfg, size_t *bytes) {
+    DenseProblem p;
+    const bsa_status st = make_cross(cfg, &p);
+    if (st != BSA_OK) return st;
+    if (!bytes) return BSA_ERR_INVALID_ARG;
+    const KeySet s = cross_set(cfg, nullptr, nullptr, nullptr);
+    *bytes = fwd_bytes(p, &s, 1);
+    return BSA_OK;
+}
+
+bsa_status bsa_cross_attention(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
+                               const int32_t *key_len, void *out, float *lse, void *out_low, void *workspace,
+                               size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream) {
+    return cross_forward(cfg, q, k, v, key_len, out, lse, out_low, workspace, workspace_bytes, status_word, stream, -1);
+}
+
+bsa_status bsa_cross_backward_workspace_size(const bsa_cross_config *cfg, size_t *bytes) {
+    DenseProblem p;
+    const bsa_status st = make_cross(cfg, &p);
+    if (st != BSA_OK) return st;
+    if (!bytes) return BSA_ERR_INVALID_ARG;
+    *bytes = bwd_bytes(p, cross_set(cfg, nullptr, nullptr, nullptr));
+    return BSA_OK;
+}
+
+bsa_status bsa_cross_attention_backward(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
+                                        const int32_t *key_len, const void *out, const float *lse, const void *out_low,
+                                        const void *dout, void *dq, void *dk, void *dv, void *workspace,
+                                        size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream) {
+    return cross_backward(cfg, q, k, v, key_len, out, lse, out_low, dout, dq, dk, dv, workspace, workspace_bytes, status_word, stream, -1);
+}
+
+bsa_status bsa_prefix_workspace_size(const bsa_prefix_config *cfg, size_t *bytes) {
+    DenseProblem p;
+    const bsa_status st = make_prefix(cfg, &p);
+    if (st != BSA_OK) return st;
+    if (!bytes) return BSA_ERR_INVALID_ARG;
+    KeySet sets[2];
+    prefix_sets(cfg, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, sets);
+    *bytes = fwd_bytes(p, sets, 2);
+    return BSA_OK;
+}
+
+bsa_status bsa_prefix_attention(const bsa_prefix_config *cfg, const void *q, const void *k_prefix, const void *v_prefix,
+                                const int32_t *prefix_len, const void *k_own, const void *v_own, const int32_t *own_len,
+                                void *out, void *workspace, size_t workspace_bytes, uint32_t *status_word,
+                                cudaStream_t stream) {
+    return prefix_forward(cfg, q, k_prefix, v_prefix, prefix_len, k_own, v_own, own_len, out, workspace, workspace_bytes, status_word, stream, -1);
+}
+
+// Test hooks (include/bsa_testing.h): the same with a copy withheld, so that bounded waits expire on purpose.
+
+bsa_status bsa_testing_cross_attention_withhold(const bsa_cross_config *cfg, const void *q, const void *k, const void *v,
+                                                const int32_t *key_len, void *out, float *lse, void *out_low,
+                                                void *workspace, size_t workspace_bytes, uint32_t *status_word,
+                                                cudaStream_t stream, int64_t withhold) {
+    if (!status_word || withhold < 0) return BSA_ERR_INVALID_ARG;
+    return cross_forward(cfg, q, k, v, key_len, out, lse, out_low, workspace, workspace_bytes, status_word, stream, withhold);
+}
+
+bsa_status bsa_testing_cross_attention_backward_withhold(const bsa_cross_config *cfg, const void *q, const void *k,
+                                                         const void *v, const int32_t *key_len, const void *out,
+                                                         const float *lse, const void *out_low, const void *dout,
+                                                         void *dq, void *dk, void *dv, void *workspace,
+                                                         size_t workspace_bytes, uint32_t *status_word,
+                                                         cudaStream_t stream, int64_t withhold) {
+    if (!status_word || withhold < 0) return BSA_ERR_INVALID_ARG;
+    return cross_backward(cfg, q, k, v, key_len, out, lse, out_low, dout, dq, dk, dv, workspace, workspace_bytes, status_word, stream, withhold);
+}
+
+bsa_status bsa_testing_prefix_attention_withhold(const bsa_prefix_config *cfg, const void *q, const void *k_prefix,
+                                                 const void *v_prefix, const int32_t *prefix_len, const void *k_own,
+                                                 const void *v_own, const int32_t *own_len, void *out, void *workspace,
+                                                 size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream,
+                                                 int64_t withhold) {
+    if (!status_word || withhold < 0) return BSA_ERR_INVALID_ARG;
+    return prefix_forward(cfg, q, k_prefix, v_prefix, prefix_len, k_own, v_own, own_len, out, workspace, workspace_bytes, status_word, stream, withhold);
 }
 
 }  // extern "C"

@@ -83,6 +83,7 @@ struct BwdParams {
     int cta0;               // first block of this pass in the launch
     float scale, scale_log2;
     uint32_t *status;
+    int64_t withhold;       // test hook
 };
 __device__ __forceinline__ int this_cta(const BwdParams &p) { return (int)blockIdx.x - p.cta0; }
 struct BwdMaps {
@@ -305,7 +306,7 @@ __device__ void copy_role(const BwdParams &p, const BwdMaps &maps, Shared<D> &sh
             const int z0 = c.cols - t * kTile, z1 = KEY ? 0 : (int)min((int64_t)kTile, p.plan.s.n - row);
             const bool zero = !KEY && z0 < z1;
             uint64_t *bar = zero ? &sh.tail : &sh.st_full[st];
-            if (leader) {
+            if (leader && !((int64_t)g == p.withhold && this_cta(p) == 0)) {
                 mbar_expect_tx(bar, 2 * C::TILE + (KEY ? kStat * 4 : 0));
                 load(sh.b0[st], &maps.b0, bar, row, (int)c.slab);
                 load(sh.b1[st], &maps.b1, bar, row, (int)c.slab);
@@ -862,6 +863,7 @@ cudaError_t launch_dense_bwd(const DenseProblem &pb, const void *q, const KeySet
     key.scale = pb.scale;
     key.scale_log2 = pb.scale * 1.4426950408889634f;
     key.status = status;
+    key.withhold = pb.withhold;
     BwdParams qry = key;
     qry.plan = plans.qry;
     qry.cta0 = plans.key.ctas;

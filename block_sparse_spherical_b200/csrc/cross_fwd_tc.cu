@@ -141,6 +141,7 @@ struct FwdParams {
     int cta0;               // first block of this pass in its launch
     float scale_log2;
     uint32_t *status;       // nullable
+    int64_t withhold;       // test hook
 };
 
 __device__ __forceinline__ int this_cta(const FwdParams &p) { return (int)blockIdx.x - p.cta0; }
@@ -297,7 +298,7 @@ __device__ void copy_role(const FwdParams &p, const Maps &maps, Shared<D> &sh, i
             const int z0 = c.rel - t * kTile, z1 = (int)min((int64_t)kTile, s.n - row);
             const bool zero = is_v && z0 < z1;
             uint64_t *bar = zero ? &sh.tail : &sh.kv_full[st];
-            if (leader) {
+            if (leader && !((int64_t)pos == p.withhold && this_cta(p) == 0)) {
                 mbar_expect_tx(bar, C::TILE);
                 for (int h = 0; h < C::HALVES; ++h)
                     tma_load_3d(sh.kv[st] + h * (kTile * 128), map, bar, 64 * h, row, slab);
@@ -1096,8 +1097,9 @@ __global__ void __launch_bounds__(256, D == 64 || ROWS == 1 ? 4 : 2) join_sets_k
             i = r % kTile;
         }
         const int2 span = p.spans[z * s.upz + hk * s.pairs + t / 2];
-        // (after an expired wait a span may be missing; what it holds then must not lead out of the parts)
-        if (span.x >= 0 && span.y >= span.x && span.y < p.plan.ctas) {
+        // (after an expired wait a span may be missing; what it holds then must not lead out of the parts, of
+        // which a set whose units are whole has none)
+        if (span.x >= 0 && span.y >= span.x && span.y < p.plan.ctas && (p.plan.stream || span.y == span.x)) {
             count = span.y - span.x + 1;
             ca = span.x;
             at = (int)(i + kTile * (t & 1));
@@ -1303,6 +1305,7 @@ cudaError_t launch_dense_fwd(const DenseProblem &pb, const void *q, const KeySet
         x.all_rows = pb.batch * pb.kv_heads * pb.rows;
         x.scale_log2 = pb.scale * 1.4426950408889634f;
         x.status = status;
+        x.withhold = pb.withhold;
         ws += L.total;
     }
     return pb.d == 64 ? run<64>(pb, q, sets, nsets, p, stream) : run<128>(pb, q, sets, nsets, p, stream);

@@ -1,5 +1,5 @@
 /*
- * bsa_testing.h — test-only entry point of libbsa.so. Not part of the BSA
+ * bsa_testing.h — test-only entry points of libbsa.so. Not part of the BSA
  * method and not for production use.
  */
 #ifndef BSA_TESTING_H
@@ -26,6 +26,32 @@ BSA_API bsa_status bsa_testing_fine_attention_withhold(const bsa_config *cfg, co
                                                        const float *o_cg_block, const int32_t *sel_idx,
                                                        void *out, uint32_t *status_word,
                                                        int64_t withhold_v_step, cudaStream_t stream);
+
+/*
+ * bsa_cross_attention, bsa_cross_attention_backward and bsa_prefix_attention
+ * with one copy deliberately not issued: the one of number `withhold` (>= 0) of
+ * the first CTA of each pass, counted over that CTA's key and value tiles (the
+ * backward: over the pairs of tiles of its steps). Waits expire after their
+ * bound (about 2 s); the kernel records BSA_ERR_TIMEOUT in *status_word
+ * (required, zero before the call), drains its copies and MMAs, frees its tensor
+ * memory and returns, and the kernels behind it run on what there is. Results
+ * are left incomplete; nothing outside of them and the workspace is touched.
+ * A number past the CTA's last copy changes nothing.
+ */
+BSA_API bsa_status bsa_testing_cross_attention_withhold(const bsa_cross_config *cfg, const void *q, const void *k,
+                                                        const void *v, const int32_t *key_len, void *out, float *lse,
+                                                        void *out_low, void *workspace, size_t workspace_bytes,
+                                                        uint32_t *status_word, cudaStream_t stream, int64_t withhold);
+BSA_API bsa_status bsa_testing_cross_attention_backward_withhold(
+    const bsa_cross_config *cfg, const void *q, const void *k, const void *v, const int32_t *key_len, const void *out,
+    const float *lse, const void *out_low, const void *dout, void *dq, void *dk, void *dv, void *workspace,
+    size_t workspace_bytes, uint32_t *status_word, cudaStream_t stream, int64_t withhold);
+BSA_API bsa_status bsa_testing_prefix_attention_withhold(const bsa_prefix_config *cfg, const void *q,
+                                                         const void *k_prefix, const void *v_prefix,
+                                                         const int32_t *prefix_len, const void *k_own,
+                                                         const void *v_own, const int32_t *own_len, void *out,
+                                                         void *workspace, size_t workspace_bytes,
+                                                         uint32_t *status_word, cudaStream_t stream, int64_t withhold);
 
 /*
  * y[i] = 2^x[i] (n device floats) as the fine-attention kernel's softmax forms
